@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_HERE, "libhils.so")
 
 HILS_F32, HILS_BF16 = 0, 1
 OP_SELECT, OP_ATTEND, OP_DECODE, OP_ATTEND_SELECTED, OP_BACKWARD = 0, 1, 2, 3, 4
+OP_DECODE_DENSE, OP_APPEND = 5, 6
 STATUS = {
     0: "HILS_OK", 1: "HILS_ERR_INVALID_ARG", 2: "HILS_ERR_UNSUPPORTED", 3: "HILS_ERR_WORKSPACE",
     4: "HILS_ERR_CUDA", 5: "HILS_ERR_DEVICE_CHECK", 6: "HILS_ERR_DEVICE_TIMEOUT",
@@ -39,6 +40,15 @@ class Shape(ctypes.Structure):
         ("top_k", ctypes.c_int32), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32),
         ("window", ctypes.c_int32),
     ]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 _lib = None
@@ -72,6 +82,9 @@ def lib():
         "hils_device_status": (i32, [_P, _P]),
         "hils_set_wait_limit": (ctypes.c_uint32, [ctypes.c_uint32]),
         "hils_backward": (i32, [S, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, sz, _P]),
+        "hils_rotate": (i32, [S, _P, _P, _P, _P, ctypes.c_int64, i32, _P, _P, i32, _P]),
+        "hils_append_paged": (i32, [S, _P, _P, _P, _P, i32, _P, _P, _P, _P, i32, i32, _P, _P, _P, _P, _P, sz, _P]),
+        "hils_decode_dense": (i32, [S, _P, _P, _P, _P, i32, _P, i32, _P, _P, _P, sz, _P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -81,8 +94,9 @@ def lib():
     return L
 
 
-EXPORTED = ["hils_abi_version", "hils_attend", "hils_attend_selected", "hils_backward", "hils_decode",
-            "hils_decode_ex", "hils_decode_static", "hils_device_status", "hils_summarize_paged_ex", "hils_select", "hils_set_wait_limit",
+EXPORTED = ["hils_abi_version", "hils_append_paged", "hils_attend", "hils_attend_selected", "hils_backward",
+            "hils_decode", "hils_decode_dense", "hils_decode_ex", "hils_decode_static", "hils_device_status",
+            "hils_rotate", "hils_summarize_paged_ex", "hils_select", "hils_set_wait_limit",
             "hils_status_string", "hils_summarize", "hils_summarize_paged", "hils_workspace_size"]
 
 DEFAULT_WAIT_LIMIT = 1 << 26  # HILS_DEFAULT_WAIT_LIMIT
@@ -441,3 +455,348 @@ def backward(q, k, v, landmark, out, lse, topk_idx, topk_score, dout, scale=None
                                _ptr(topk_idx), _ptr(topk_score), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
                                _ptr(dl), _ptr(ws), ws.numel(), _stream(stream)), "hils_backward")
     return dq, dk, dv, dl
+
+
+# ---- the paged cache around the method: rotation, appended tokens, dense layers ----
+
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+class _on:
+    """Makes the device of tensor t current (kernels launch on the current device) and, if
+    `stream` is given, that stream (so that what the call allocates belongs to it); gives
+    the raw stream to launch on.  The tensor must be on a GPU."""
+
+    def __init__(self, t, stream):
+        if not t.is_cuda:
+            raise ValueError("tensors must be on a CUDA device")
+        if stream is not None and stream.device != t.device:
+            raise ValueError("stream must be of the tensors' device")
+        self.stream = stream
+        self.dev = t.device.index
+        self.ctx = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+            return self.stream.cuda_stream
+        self.prev = torch.cuda.current_device()
+        if self.prev != self.dev:
+            torch.cuda.set_device(self.dev)
+        return torch.cuda.current_stream(self.dev).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        elif self.prev != self.dev:
+            torch.cuda.set_device(self.prev)
+        return False
+
+
+def _own_workspace(shape, op, device, ws):
+    """ws checked, or a new workspace whose zeroes are in place before any stream uses it."""
+    if ws is not None:
+        if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.numel() < max(256, workspace_size(shape, op)):
+            raise ValueError("ws must be a contiguous uint8 tensor of workspace_size bytes")
+        return ws
+    ws = new_workspace(shape, op, device)
+    if ws.is_cuda and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(ws.device).synchronize()
+    return ws
+
+
+def _dense_shape(batch, heads_q, heads_kv, head_dim, max_chunks, dtype, scale=None, window=0):
+    if max_chunks * 64 >= 1 << 31:
+        raise ValueError("max_chunks * 64 must stay below 2**31")
+    return make_shape(batch, heads_q, heads_kv, head_dim, max_chunks * 64, 0,
+                      HILS_BF16 if dtype in (torch.bfloat16, "bf16") else HILS_F32, scale=scale or 0.0, window=window)
+
+
+def _rows(t, name, packed=False):
+    """t as hils_rows: [b, heads, n, d], or packed [tokens, heads, d]; any strides whose rows
+    are 16-byte aligned and contiguous."""
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    st = [x if n > 1 else 0 for x, n in zip(t.stride(), t.shape)]  # a single entry needs no stride
+    r = Rows(t.data_ptr(), 0, st[1], st[0]) if packed else Rows(t.data_ptr(), st[0], st[1], st[2])
+    e = t.element_size()
+    if ((r.data or 0) | r.batch_stride * e | r.head_stride * e | r.token_stride * e) & 15:
+        raise ValueError(f"{name}: rows must be 16-byte aligned (data pointer and strides)")
+    return r
+
+
+def _span(t):
+    """First and last byte address of t's elements (t is not empty)."""
+    n = sum((x - 1) * s for x, s in zip(t.shape, t.stride()))
+    p = t.data_ptr()
+    return p, p + (n + 1) * t.element_size() - 1
+
+
+def _check_written(out, name, *others, itself=None):
+    """A written tensor is contiguous memory apart from the others, or `itself` in place."""
+    if itself is not None and out.data_ptr() == itself.data_ptr() and out.stride() == itself.stride() \
+            and out.dtype == itself.dtype:
+        if any(s == 0 and n > 1 for n, s in zip(out.shape, out.stride())):
+            raise ValueError(f"{name}: an expanded tensor cannot be written in place")
+    elif not out.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, or its input itself")
+    else:
+        others = (*others, itself)
+    if out.numel() == 0:
+        return
+    a0, a1 = _span(out)
+    for t in others:
+        if t is not None and t.numel():
+            b0, b1 = _span(t)
+            if a0 <= b1 and b0 <= a1:
+                raise ValueError(f"{name} overlaps another tensor of the call")
+
+
+def _rope(inv_freq, interleaved, d):
+    if inv_freq is None:
+        return None
+    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous():
+        raise TypeError("inv_freq must be a contiguous fp32 vector")
+    r = 2 * inv_freq.numel()
+    if r == 0 or r > d or r % 16:
+        raise ValueError(f"inv_freq must have a multiple of 8 entries, at most head_dim / 2; got {r // 2}")
+    return Rope(inv_freq.data_ptr(), r, 1 if interleaved else 0)
+
+
+def check_rotate_args(q, inv_freq, k=None, positions=None, q_out=None, k_out=None):
+    """The tensors of rotate against one another; returns the stride of positions over the
+    batch (0: shared)."""
+    if q.dim() != 4:
+        raise ValueError("q must be [b, heads_q, n, d]")
+    b, _, n, d = q.shape
+    if q.dtype not in _FLOATS:
+        raise TypeError(f"q must be bf16 or fp32, got {q.dtype}")
+    if inv_freq is None:
+        raise ValueError("inv_freq is required")
+    out_dtypes = _FLOATS
+    if q_out is not None:
+        _expect(q_out, q.shape, _FLOATS, "q_out")
+        _check_written(q_out, "q_out", k, positions, inv_freq, itself=q)
+        out_dtypes = (q_out.dtype,)
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError("k must be [b, heads_kv, n, d]")
+        _expect(k, (b, k.shape[1], n, d), (q.dtype,), "k")
+        if k_out is not None:
+            _expect(k_out, k.shape, out_dtypes if q_out is not None else (q.dtype,), "k_out")
+            _check_written(k_out, "k_out", q, q_out, positions, inv_freq, itself=k)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _same_device(q, inv_freq, k, positions, q_out, k_out)
+    if positions is None:
+        return 0
+    if positions.dtype != torch.int32 or not positions.is_contiguous():
+        raise TypeError("positions must be contiguous int32")
+    if positions.shape == (n,):
+        return 0
+    if positions.shape != (b, n):
+        raise ValueError("positions must be [n] or [b, n]")
+    return n
+
+
+def rotate(q, inv_freq, k=None, positions=None, inverse=False, interleaved=False, q_out=None, k_out=None,
+           stream=None):
+    """Position rotation of q [b,h,n,d] (and k [b,g,n,d]); returns q_out, or (q_out, k_out).
+
+    inv_freq [rotary_dim / 2] fp32: frequency f turns pair f by position * inv_freq[f]; pair f
+    is (f, f + rotary_dim / 2), or (2f, 2f + 1) when interleaved; elements from rotary_dim on
+    are copied.  positions: None (token i at position i), int32 [n], or int32 [b, n].
+    inverse: the opposite rotation, which takes the gradients of the rotated q and k (backward's
+    dq and dk) to those of the unrotated ones.  q and k may be slices with any strides whose rows
+    are 16-byte aligned; an output may be its input (in place), and may be bf16 or fp32."""
+    pstride = check_rotate_args(q, inv_freq, k, positions, q_out, k_out)
+    b, h, n, d = q.shape
+    rope = _rope(inv_freq, interleaved, d)
+    ref = ctypes.byref
+    with _on(q, stream) as st:
+        if q_out is None:
+            q_out = torch.empty((b, h, n, d), dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=q_out.dtype, device=q.device)
+        if q_out.numel() and (k is None or k.numel()):
+            sh = make_shape(b, h, h if k is None else k.shape[1], d, n, 0, _dt(q))
+            _check(lib().hils_rotate(ref(sh), ref(_rows(q, "q")), None if k is None else ref(_rows(k, "k")), ref(rope),
+                                     None if positions is None else positions.data_ptr(), pstride,
+                                     1 if inverse else 0, ref(_rows(q_out, "q_out")),
+                                     None if k is None else ref(_rows(k_out, "k_out")), _dt(q_out), st),
+                   "hils_rotate")
+    return q_out if k is None else (q_out, k_out)
+
+
+def append_slots(batch, tokens):
+    """Entries of Append's full_pages for a call of `tokens` rows in all (batch * n for
+    [b, heads, n, d])."""
+    return batch + tokens // 64
+
+
+def check_append_args(shape, k, v, k_pages, v_pages, block_table, max_chunks, seq_lens, q=None, q_out=None,
+                      cu_new=None, new_lens=None, full_pages=None):
+    """The tensors of an append against the shape (see Append.__call__)."""
+    b, h, g, d = shape.batch, shape.heads_q, shape.heads_kv, shape.head_dim
+    dts = (torch.bfloat16 if shape.dtype == HILS_BF16 else torch.float32,)
+    if k.dim() == 3:
+        n = tokens = k.shape[0]
+        rows, qrows = (n, g, d), (n, h, d)
+        if cu_new is not None:
+            _expect(cu_new, (b + 1,), (torch.int32,), "cu_new")
+        elif n != b:
+            raise ValueError("packed tokens need cu_new unless there is one per sequence")
+        if new_lens is not None:
+            raise ValueError("new_lens goes with [b, heads, n, d] tokens")
+    elif k.dim() == 4:
+        n = k.shape[2]
+        tokens = b * n
+        rows, qrows = (b, g, n, d), (b, h, n, d)
+        if cu_new is not None:
+            raise ValueError("cu_new goes with packed [tokens, heads, d] rows")
+        if new_lens is not None:
+            _expect(new_lens, (b,), (torch.int32,), "new_lens")
+    else:
+        raise ValueError("k must be [b, heads_kv, n, d] or [tokens, heads_kv, d]")
+    _expect(k, rows, dts, "k")
+    _expect(v, rows, dts, "v")
+    P = k_pages.shape[0] if k_pages.dim() == 4 else -1
+    _expect(k_pages, (P, g, 64, d), dts, "k_pages")
+    _expect(v_pages, (P, g, 64, d), dts, "v_pages")
+    _expect(block_table, (b, max_chunks), (torch.int32,), "block_table")
+    _expect(seq_lens, (b,), (torch.int32,), "seq_lens")
+    if q is not None:
+        _expect(q, qrows, dts, "q")
+        if q_out is not None:
+            _expect(q_out, qrows, dts, "q_out")
+            _check_written(q_out, "q_out", k, v, k_pages, v_pages, itself=q)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if full_pages is not None:
+        _expect(full_pages, (append_slots(b, tokens),), (torch.int32,), "full_pages")
+    _same_device(k, v, q, q_out, k_pages, v_pages, block_table, seq_lens, cu_new, new_lens, full_pages)
+
+
+class Append:
+    """Reusable call that writes new tokens into a paged cache of `max_chunks` chunks per
+    sequence; holds the rotation (inv_freq, see rotate; None: no rotation) and the error
+    word (`ws`: the caller's own zero-filled workspace)."""
+
+    def __init__(self, batch, heads_q, heads_kv, head_dim, max_chunks, dtype, inv_freq=None, interleaved=False,
+                 device="cuda", ws=None):
+        self.max_chunks = max_chunks
+        self.shape = _dense_shape(batch, heads_q, heads_kv, head_dim, max_chunks, dtype)
+        self.inv_freq = inv_freq
+        self.rope = _rope(inv_freq, interleaved, head_dim)
+        self.ws = _own_workspace(self.shape, OP_APPEND, device, ws)
+        _same_device(self.ws, inv_freq)
+
+    def __call__(self, k, v, k_pages, v_pages, block_table, seq_lens, q=None, q_out=None, cu_new=None, new_lens=None,
+                 full_pages=None, stream=None):
+        """Writes k, v into k_pages, v_pages [P,g,64,d] (the keys rotated by their position);
+        returns q_out, the rotated queries, or None.
+
+        k, v [b,g,n,d] with q [b,h,n,d]: n tokens per sequence, of which new_lens [b] int32 may
+        take only the first ones (right padding).  k, v [tokens,g,d] with q [tokens,h,d]: packed;
+        cu_new [b+1] int32 gives each sequence's rows, or None: one token per sequence.
+        seq_lens [b] int32 are the lengths after the call.  full_pages: int32
+        [append_slots(b, tokens)], receives the pages filled by the call, else -1: it can go to
+        summarize_paged as it is."""
+        s = self.shape
+        check_append_args(s, k, v, k_pages, v_pages, block_table, self.max_chunks, seq_lens, q, q_out, cu_new,
+                          new_lens, full_pages)
+        _same_device(k, self.ws)
+        ref = ctypes.byref
+        packed = cu_new is not None
+        single = k.dim() == 3 and not packed  # one token per sequence: [b, heads, 1, d]
+
+        def rows_of(t, name):
+            return None if t is None else ref(_rows(t.unsqueeze(2) if single else t, name, packed))
+
+        with _on(k, stream) as st:
+            if q is not None and q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            _check(lib().hils_append_paged(
+                ref(s), rows_of(k, "k"), rows_of(v, "v"), rows_of(q, "q"), rows_of(q_out, "q_out"),
+                1 if single else k.shape[0] if packed else k.shape[2], _ptr(cu_new), _ptr(new_lens), _ptr(seq_lens),
+                _ptr(block_table), self.max_chunks, k_pages.shape[0], None if self.rope is None else ref(self.rope),
+                _ptr(k_pages), _ptr(v_pages), _ptr(full_pages), _ptr(self.ws), self.ws.numel(), st),
+                "hils_append_paged")
+        return q_out
+
+    def device_status(self, stream=None):
+        with _on(self.ws, stream) as st:
+            return lib().hils_device_status(_ptr(self.ws), st)
+
+
+def append_paged(k, v, k_pages, v_pages, block_table, seq_lens, inv_freq=None, interleaved=False, q=None, q_out=None,
+                 cu_new=None, new_lens=None, full_pages=None, stream=None):
+    """Append for one call (see Append.__call__); device-side errors are not reported."""
+    b, max_chunks = block_table.shape
+    g, d = k_pages.shape[1], k_pages.shape[3]
+    with _on(k, stream):
+        sh = _dense_shape(b, g if q is None else q.shape[1], g, d, max_chunks, k_pages.dtype)
+        call = Append(b, sh.heads_q, g, d, max_chunks, k_pages.dtype, inv_freq=inv_freq, interleaved=interleaved,
+                      ws=new_workspace(sh, OP_APPEND, k.device))
+        return call(k, v, k_pages, v_pages, block_table, seq_lens, q=q, q_out=q_out, cu_new=cu_new,
+                    new_lens=new_lens, full_pages=full_pages)
+
+
+def check_dense_args(shape, q, k_pages, v_pages, block_table, max_chunks, seq_lens, out=None, lse=None):
+    """The tensors of a dense decode against the shape: q [b,h,d]; k/v pages [P,g,64,d] in q's
+    dtype; block_table [b, max_chunks] and seq_lens [b] int32; out like q; lse [b,h] fp32."""
+    b, h, d = shape.batch, shape.heads_q, shape.head_dim
+    dts = (torch.bfloat16 if shape.dtype == HILS_BF16 else torch.float32,)
+    _expect(q, (b, h, d), dts, "q")
+    pages = (k_pages.shape[0] if k_pages.dim() == 4 else -1, shape.heads_kv, 64, d)
+    _expect(k_pages, pages, dts, "k_pages")
+    _expect(v_pages, pages, dts, "v_pages")
+    _expect(block_table, (b, max_chunks), (torch.int32,), "block_table")
+    _expect(seq_lens, (b,), (torch.int32,), "seq_lens")
+    if out is not None:
+        _expect(out, (b, h, d), dts, "out")
+    if lse is not None:
+        _expect(lse, (b, h), (torch.float32,), "lse")
+    _same_device(q, k_pages, v_pages, block_table, seq_lens, out, lse)
+
+
+class DenseDecode:
+    """Reusable decode call of a dense layer (every key, or a sliding window of chunks) for a
+    paged cache of `max_chunks` chunks per sequence; holds the workspace, which serves one
+    call at a time (`ws`: the caller's own, zero-filled)."""
+
+    def __init__(self, batch, heads_q, heads_kv, head_dim, max_chunks, dtype, scale=None, device="cuda", window=0,
+                 ws=None):
+        self.max_chunks = max_chunks
+        self.shape = _dense_shape(batch, heads_q, heads_kv, head_dim, max_chunks, dtype, scale, window)
+        self.ws = _own_workspace(self.shape, OP_DECODE_DENSE, device, ws)
+
+    def __call__(self, q, k_pages, v_pages, block_table, seq_lens, out=None, lse=None, stream=None):
+        """out [b,h,d] (q's dtype); lse, if given (fp32 [b,h]), receives log sum exp(logit)."""
+        check_dense_args(self.shape, q, k_pages, v_pages, block_table, self.max_chunks, seq_lens, out, lse)
+        _same_device(q, self.ws)
+        with _on(q, stream) as st:
+            if out is None:
+                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            _check(lib().hils_decode_dense(ctypes.byref(self.shape), _ptr(q), _ptr(k_pages), _ptr(v_pages),
+                                           _ptr(block_table), self.max_chunks, _ptr(seq_lens), k_pages.shape[0],
+                                           _ptr(out), _ptr(lse), _ptr(self.ws), self.ws.numel(), st),
+                   "hils_decode_dense")
+        return out
+
+    def device_status(self, stream=None):
+        with _on(self.ws, stream) as st:
+            return lib().hils_device_status(_ptr(self.ws), st)
+
+
+def decode_dense(q, k_pages, v_pages, block_table, seq_lens, scale=None, window=0, return_lse=False, stream=None):
+    """Attention of one new token per sequence over every key of its pages (window 0), or the
+    last window / 64 chunks; returns out [b,h,d], then lse [b,h] when asked."""
+    b, h, d = q.shape
+    with _on(q, stream):
+        sh = _dense_shape(b, h, k_pages.shape[1], d, block_table.shape[1], q.dtype, scale, window)
+        call = DenseDecode(b, h, k_pages.shape[1], d, block_table.shape[1], q.dtype, scale=scale, window=window,
+                           ws=new_workspace(sh, OP_DECODE_DENSE, q.device))
+        lse = torch.empty((b, h), dtype=torch.float32, device=q.device) if return_lse else None
+        out = call(q, k_pages, v_pages, block_table, seq_lens, lse=lse)
+    return (out, lse) if return_lse else out

@@ -197,6 +197,23 @@ cudaError_t run_prefill_attention(const hils_shape* s, const void* q, const void
   return hils::run_attend_rows(ar, cs);
 }
 
+// Rows that 16-byte loads and stores can take.
+hils_status check_rows(const hils_rows* r, size_t elem) {
+  if (!r || !r->data) return HILS_ERR_INVALID_ARG;
+  if (!aligned16(r->data) || r->batch_stride * (long long)elem % 16 != 0 || r->head_stride * (long long)elem % 16 != 0 ||
+      r->token_stride * (long long)elem % 16 != 0)
+    return HILS_ERR_INVALID_ARG;
+  return HILS_OK;
+}
+hils_status check_rope(const hils_rope* r, int head_dim) {
+  if (!r || !r->inv_freq || (reinterpret_cast<uintptr_t>(r->inv_freq) & 3u) != 0) return HILS_ERR_INVALID_ARG;
+  if (r->rotary_dim <= 0 || r->rotary_dim > head_dim || (r->interleaved != 0 && r->interleaved != 1))
+    return HILS_ERR_INVALID_ARG;
+  return r->rotary_dim % 16 == 0 ? HILS_OK : HILS_ERR_UNSUPPORTED;
+}
+hils::Rows rows_of(const hils_rows* r) { return {r->data, r->batch_stride, r->head_stride, r->token_stride}; }
+size_t elem_size(int32_t dtype) { return dtype == HILS_BF16 ? 2 : 4; }
+
 }  // namespace
 
 extern "C" {
@@ -228,6 +245,8 @@ hils_status hils_workspace_size(const hils_shape* s, int32_t op, size_t* bytes) 
     case HILS_OP_DECODE: *bytes = decode_layout(s).total; return HILS_OK;
     case HILS_OP_ATTEND_SELECTED: *bytes = kHeader + cm_bytes(s); return HILS_OK;
     case HILS_OP_BACKWARD: *bytes = backward_layout(s).total; return HILS_OK;
+    case HILS_OP_DECODE_DENSE: *bytes = kHeader; return HILS_OK;
+    case HILS_OP_APPEND: *bytes = kHeader; return HILS_OK;
   }
   return HILS_ERR_INVALID_ARG;
 }
@@ -455,6 +474,93 @@ hils_status hils_decode_ex(const hils_shape* s, const void* q, const void* k_pag
   da.kbar_bf16 = summary_dtype == HILS_BF16;
   da.n_local = n_local(s);
   return cuda_status(hils::run_decode(da, cs));
+}
+
+hils_status hils_rotate(const hils_shape* s, const hils_rows* q, const hils_rows* k, const hils_rope* rope,
+                        const int32_t* positions, int64_t position_stride, int32_t inverse, const hils_rows* q_out,
+                        const hils_rows* k_out, int32_t out_dtype, void* stream) {
+  hils_status st = check_shape(s, true);
+  if (st != HILS_OK) return st;
+  if (out_dtype != HILS_F32 && out_dtype != HILS_BF16) return HILS_ERR_INVALID_ARG;
+  if ((k == nullptr) != (k_out == nullptr)) return HILS_ERR_INVALID_ARG;
+  if (position_stride < 0) return HILS_ERR_INVALID_ARG;
+  if ((st = check_rope(rope, s->head_dim)) != HILS_OK) return st;
+  if ((size_t)s->batch * s->seq_len == 0) return HILS_OK;
+  if ((st = check_rows(q, elem_size(s->dtype))) != HILS_OK || (st = check_rows(q_out, elem_size(out_dtype))) != HILS_OK)
+    return st;
+  if (k && ((st = check_rows(k, elem_size(s->dtype))) != HILS_OK ||
+            (st = check_rows(k_out, elem_size(out_dtype))) != HILS_OK))
+    return st;
+  hils::RotateArgs a{};
+  a.in[0] = rows_of(q); a.out[0] = rows_of(q_out); a.heads[0] = s->heads_q;
+  if (k) { a.in[1] = rows_of(k); a.out[1] = rows_of(k_out); a.heads[1] = s->heads_kv; }
+  a.inv_freq = rope->inv_freq; a.rot = rope->rotary_dim; a.interleaved = rope->interleaved != 0;
+  a.positions = positions; a.position_stride = position_stride; a.inverse = inverse != 0;
+  a.b = s->batch; a.n = s->seq_len; a.d = s->head_dim;
+  a.in_bf16 = s->dtype == HILS_BF16; a.out_bf16 = out_dtype == HILS_BF16;
+  return cuda_status(hils::run_rotate(a, (cudaStream_t)stream));
+}
+
+hils_status hils_append_paged(const hils_shape* s, const hils_rows* k, const hils_rows* v, const hils_rows* q,
+                              const hils_rows* q_out, int32_t n_new, const int32_t* cu_new,
+                              const int32_t* new_lens, const int32_t* seq_lens, const int32_t* block_table,
+                              int32_t max_chunks, int32_t n_pages, const hils_rope* rope, void* k_pages,
+                              void* v_pages, int32_t* full_pages, void* ws, size_t ws_bytes, void* stream) {
+  hils_status st = check_shape(s, false);
+  if (st != HILS_OK) return st;
+  if (n_new < 0 || (q == nullptr) != (q_out == nullptr) || (cu_new && new_lens)) return HILS_ERR_INVALID_ARG;
+  if (rope && (st = check_rope(rope, s->head_dim)) != HILS_OK) return st;
+  const long long tokens = cu_new ? n_new : (long long)s->batch * n_new;
+  if (s->batch == 0) return HILS_OK;
+  if (tokens > 0x7fffffffll) return HILS_ERR_UNSUPPORTED;
+  if (max_chunks <= 0 || n_pages <= 0) return HILS_ERR_INVALID_ARG;
+  if (max_chunks > (0x7fffffff / s->chunk)) return HILS_ERR_UNSUPPORTED;  // positions are 32-bit
+  if (!seq_lens || !block_table) return HILS_ERR_INVALID_ARG;
+  const size_t es = elem_size(s->dtype);
+  if (tokens > 0) {
+    if (!k_pages || !v_pages || !aligned16(k_pages) || !aligned16(v_pages)) return HILS_ERR_INVALID_ARG;
+    if ((st = check_rows(k, es)) != HILS_OK || (st = check_rows(v, es)) != HILS_OK) return st;
+    if (q && ((st = check_rows(q, es)) != HILS_OK || (st = check_rows(q_out, es)) != HILS_OK)) return st;
+  } else if (!full_pages) {
+    return HILS_OK;
+  }
+  if (!ws || ws_bytes < kHeader || !aligned16(ws)) return HILS_ERR_WORKSPACE;
+  hils::AppendArgs a{};
+  if (tokens > 0) {
+    a.k = rows_of(k); a.v = rows_of(v);
+    if (q) { a.q = rows_of(q); a.q_out = rows_of(q_out); a.h = s->heads_q; }
+  }
+  a.g = s->heads_kv; a.b = s->batch; a.d = s->head_dim; a.n_new = n_new;
+  a.cu_new = cu_new; a.new_lens = new_lens; a.seq_lens = seq_lens; a.block_table = block_table;
+  a.max_chunks = max_chunks; a.n_pages = n_pages;
+  if (rope) { a.inv_freq = rope->inv_freq; a.rot = rope->rotary_dim; a.interleaved = rope->interleaved != 0; }
+  a.bf16 = s->dtype == HILS_BF16; a.k_pages = k_pages; a.v_pages = v_pages;
+  a.full_pages = full_pages;
+  const long long slots = s->batch + tokens / s->chunk;
+  if (slots > 0x7fffffffll) return HILS_ERR_UNSUPPORTED;
+  a.n_slots = full_pages ? (int)slots : 0;
+  a.err = static_cast<unsigned*>(ws);
+  return cuda_status(hils::run_append(a, (cudaStream_t)stream));
+}
+
+hils_status hils_decode_dense(const hils_shape* s, const void* q, const void* k_pages, const void* v_pages,
+                              const int32_t* block_table, int32_t max_chunks, const int32_t* seq_lens,
+                              int32_t n_pages, void* out, float* lse_out, void* ws, size_t ws_bytes, void* stream) {
+  hils_status st = check_shape(s, true);
+  if (st != HILS_OK) return st;
+  if (s->batch == 0) return HILS_OK;
+  if (max_chunks <= 0 || n_pages <= 0) return HILS_ERR_INVALID_ARG;
+  if ((long long)max_chunks > ((long long)s->seq_len + s->chunk - 1) / s->chunk) return HILS_ERR_INVALID_ARG;
+  if (!q || !k_pages || !v_pages || !block_table || !seq_lens || !out) return HILS_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out)) return HILS_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < kHeader || !aligned16(ws)) return HILS_ERR_WORKSPACE;
+  hils::DenseArgs a{};
+  a.q = q; a.k_pages = k_pages; a.v_pages = v_pages; a.block_table = block_table; a.seq_lens = seq_lens;
+  a.out = out; a.lse = lse_out; a.err = static_cast<unsigned*>(ws);
+  a.b = s->batch; a.h = s->heads_q; a.g = s->heads_kv; a.d = s->head_dim;
+  a.max_chunks = max_chunks; a.n_pages = n_pages; a.n_win = s->window / s->chunk;
+  a.scale = eff_scale(s); a.bf16 = s->dtype == HILS_BF16; a.poll = g_wait_limit.load();
+  return cuda_status(hils::run_decode_dense(a, (cudaStream_t)stream));
 }
 
 hils_status hils_device_status(void* ws, void* stream) {

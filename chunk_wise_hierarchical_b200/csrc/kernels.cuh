@@ -208,4 +208,60 @@ cudaError_t run_attend_tc(const TcAttendArgs& a, int d, cudaStream_t st);
 bool attend_tc3_supported(int d, int G, int K, int N);
 cudaError_t run_attend_tc3(const TcAttendArgs& a, cudaStream_t st);
 
+// Rows of d elements, one per (batch, head, token); strides in elements.
+struct Rows {
+  void* data;
+  long long batch_stride, head_stride, token_stride;
+};
+
+struct RotateArgs {
+  Rows in[2], out[2];         // q, k
+  int heads[2];               // k: 0 where there is none
+  const float* inv_freq;      // [rot / 2]
+  const int32_t* positions;   // nullptr: token i at position i
+  long long position_stride;
+  int b, n, d, rot;
+  bool interleaved, inverse, in_bf16, out_bf16;
+  int tile, head_block;       // tokens and heads of a CTA (set by the launcher)
+};
+cudaError_t run_rotate(RotateArgs a, cudaStream_t st);
+
+struct AppendArgs {
+  Rows q, q_out, k, v;
+  int h, g, b, d;             // h: 0 where no queries are rotated
+  int n_new;                  // tokens per sequence, or rows in all (cu_new)
+  const int32_t* cu_new;      // [b + 1] or nullptr
+  const int32_t* new_lens;    // [b] or nullptr
+  const int32_t* seq_lens;
+  const int32_t* block_table;
+  int max_chunks, n_pages;
+  const float* inv_freq;      // nullptr: no rotation
+  int rot;
+  bool interleaved, bf16;
+  void* k_pages;
+  void* v_pages;
+  int32_t* full_pages;        // [n_slots] or nullptr
+  int n_slots;
+  unsigned* err;
+  int tile, head_block;       // set by the launcher
+};
+cudaError_t run_append(AppendArgs a, cudaStream_t st);
+
+struct DenseArgs {
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  void* out;
+  float* lse;                 // nullptr: not written
+  unsigned* err;
+  int b, h, g, d, max_chunks, n_pages;
+  int n_win;                  // chunks of the window; 0: every chunk
+  float scale;
+  bool bf16;
+  uint32_t poll;
+};
+cudaError_t run_decode_dense(DenseArgs a, cudaStream_t st);
+
 }  // namespace hils

@@ -80,7 +80,9 @@ typedef enum {
   HILS_OP_ATTEND = 1,
   HILS_OP_DECODE = 2,
   HILS_OP_ATTEND_SELECTED = 3,
-  HILS_OP_BACKWARD = 4
+  HILS_OP_BACKWARD = 4,
+  HILS_OP_DECODE_DENSE = 5,
+  HILS_OP_APPEND = 6
 } hils_op;
 
 typedef struct {
@@ -370,6 +372,117 @@ HILS_API hils_status hils_decode_ex(const hils_shape* shape, const void* q, cons
                            int32_t max_chunks, const int32_t* seq_lens, int32_t n_pages,
                            void* out, int32_t* topk_idx_out, void* ws, size_t ws_bytes,
                            void* stream);
+
+/* ---- the paged cache around the method: rotated positions, appended tokens, dense layers.
+ * The HiLS notes leave the position scheme to the model (section 5.4 names RoPE and HoPE as
+ * such) and use full and sliding-window attention as the layers to compare with; these entry
+ * points give a caller of hils_attend / hils_backward / hils_decode the rest of the step. */
+
+/* Rows of head_dim adjacent elements, one per (batch, head, token):
+ * row = data + batch*batch_stride + head*head_stride + token*token_stride, strides in
+ * elements.  data and every stride times the element size are multiples of 16 bytes, so
+ * slices of a fused [tokens, (h + 2g) * d] projection are read where they lie. */
+typedef struct {
+  void* data;
+  int64_t batch_stride, head_stride, token_stride;
+} hils_rows;
+
+/* Position rotation.  Frequency f turns the pair f of each row's first rotary_dim elements
+ * by position * inv_freq[f] radians; the other elements are left as they are.
+ *   inv_freq     [rotary_dim / 2] fp32, device
+ *   rotary_dim   a multiple of 16, 16 <= rotary_dim <= head_dim
+ *   interleaved  0: pair f is (f, f + rotary_dim / 2); 1: pair f is (2f, 2f + 1)
+ * Angles are reduced in fp64 (position * inv_freq is exact to far below an fp32 step at any
+ * int32 position), the products are fp32, and each output is rounded once. */
+typedef struct {
+  const float* inv_freq;
+  int32_t rotary_dim;
+  int32_t interleaved;
+} hils_rope;
+
+/*
+ * hils_rotate -- rotates the rows of q (and k) by their positions: the queries and keys
+ * that hils_attend and hils_select take, from the projection that made them.  With inverse
+ * != 0 the rotation goes the other way, which is its transpose: applied to the dq and dk of
+ * hils_backward it gives the gradients of the unrotated q and k.
+ *   shape        batch, heads_q, heads_kv, head_dim, seq_len (tokens per sequence) and dtype
+ *                (of q and k) are read; the other fields must be valid
+ *   q, q_out     rows of heads_q heads
+ *   k, k_out     rows of heads_kv heads, or both NULL
+ *   positions    NULL: token i is at position i; else int32 [seq_len], or
+ *                [batch, seq_len] with position_stride = seq_len (0: shared by the batch)
+ *   out_dtype    hils_dtype of q_out and k_out
+ * An output may be its input's own memory (same data, strides and type); any other overlap
+ * is an error of the caller.
+ */
+HILS_API hils_status hils_rotate(const hils_shape* shape, const hils_rows* q, const hils_rows* k,
+                                 const hils_rope* rope, const int32_t* positions, int64_t position_stride,
+                                 int32_t inverse, const hils_rows* q_out, const hils_rows* k_out,
+                                 int32_t out_dtype, void* stream);
+
+/*
+ * hils_append_paged -- writes the keys and values of new tokens into the pages of their
+ * sequences, the keys rotated by their position in the cache on the way; optionally rotates
+ * the tokens' queries too, and lists the pages that the call fills.
+ *   shape        batch, heads_q, heads_kv, head_dim, chunk and dtype (of every tensor) are
+ *                read; the other fields must be valid
+ *   k, v         rows of heads_kv heads: the new tokens
+ *   q, q_out     rows of heads_q heads, or both NULL
+ *   n_new        cu_new == NULL: tokens per sequence of the rows' batch dimension
+ *                (token i of sequence b is row (b, head, i)); new_lens [batch] int32 may
+ *                shorten sequence b to its first new_lens[b] tokens (NULL: all n_new).
+ *                cu_new != NULL: the rows in all; the batch strides and new_lens are not
+ *                read, and sequence b owns the rows cu_new[b] <= token < cu_new[b + 1]
+ *   cu_new       [batch + 1] int32, not decreasing, or NULL; rows from cu_new[batch] on are
+ *                padding: neither read nor written
+ *   seq_lens     [batch] int32: the lengths after the call.  Token i of sequence b goes to
+ *                position seq_lens[b] - (its new tokens) + i, as hils_decode expects
+ *   block_table  [batch, max_chunks] int32: page of chunk c of sequence b
+ *   rope         NULL: keys and queries are copied unrotated
+ *   k_pages,
+ *   v_pages      [n_pages, heads_kv, B, head_dim]: rows of the new positions are written,
+ *                others untouched.  Two tokens of a call with the same page and row: which
+ *                of the two is left there is not defined
+ *   full_pages   int32 [batch + (tokens in all) / B], or NULL: the pages whose last row this
+ *                call writes, -1 in the other entries, in an order fixed by the arguments --
+ *                as it stands an argument of hils_summarize_paged, which skips the -1
+ *   ws           workspace of hils_workspace_size(HILS_OP_APPEND) bytes, zero-filled before
+ *                first use: the error word
+ * A token whose position lies outside [0, max_chunks * B), or whose page id lies outside
+ * [0, n_pages), is not written to the pages and is flagged; its query is rotated where the
+ * position is not negative.
+ */
+HILS_API hils_status hils_append_paged(const hils_shape* shape, const hils_rows* k, const hils_rows* v,
+                                       const hils_rows* q, const hils_rows* q_out, int32_t n_new,
+                                       const int32_t* cu_new, const int32_t* new_lens,
+                                       const int32_t* seq_lens, const int32_t* block_table,
+                                       int32_t max_chunks, int32_t n_pages, const hils_rope* rope,
+                                       void* k_pages, void* v_pages, int32_t* full_pages, void* ws,
+                                       size_t ws_bytes, void* stream);
+
+/*
+ * hils_decode_dense -- attention of one new token per sequence over every key of its paged
+ * cache, for the layers that do not select: the cache, block table and lengths of
+ * hils_decode, without its summaries and Top-K.
+ *   q            [batch, heads_q, head_dim] (dtype)
+ *   shape.window 0: every key.  A multiple W of B: the last W / B chunks up to the new
+ *                token, keys from (floor((seq_lens[b] - 1) / B) + 1 - W / B) * B on -- the
+ *                local branch that hils_decode takes for the same window (here W = B is the
+ *                own chunk alone, and 0 is not).  shape.top_k is not read
+ *   out          [batch, heads_q, head_dim] (dtype), written
+ *   lse_out      [batch, heads_q] fp32 or NULL: log of the sum of exp(logit) over the keys
+ *   ws           workspace of hils_workspace_size(HILS_OP_DECODE_DENSE) bytes, zero-filled
+ *                before first use; one call at a time (calls that may run at the same time,
+ *                graphs among them, take a workspace each)
+ * seq_lens[b] <= 0 gives a zero row and lse -inf, and so does a row whose every logit is
+ * -inf.  What the pages hold at and after position seq_lens[b] is not looked at: it may be
+ * anything, NaN included.  Page ids outside [0, n_pages) are skipped and flagged, and so are
+ * the keys of a length beyond max_chunks * B.
+ */
+HILS_API hils_status hils_decode_dense(const hils_shape* shape, const void* q, const void* k_pages,
+                                       const void* v_pages, const int32_t* block_table, int32_t max_chunks,
+                                       const int32_t* seq_lens, int32_t n_pages, void* out, float* lse_out,
+                                       void* ws, size_t ws_bytes, void* stream);
 
 /*
  * hils_device_status -- synchronises `stream`, reads and clears the error

@@ -1,0 +1,269 @@
+"""The paged-cache operators on the host: their oracle against closed forms, the argument
+checks of the binding (CPU tensors) and of the C ABI (nothing is launched)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import chunk_wise_hierarchical_b200 as hils
+from chunk_wise_hierarchical_b200 import _abi
+from chunk_wise_hierarchical_b200._abi import (HILS_BF16, HILS_F32, Rope, Rows, check_append_args, check_dense_args,
+                                               check_rotate_args, make_shape)
+from oracle import cache_oracle as CO
+from oracle import hils_oracle as O
+
+BF = torch.bfloat16
+P_ = ctypes.c_void_p
+FAKE = P_(1 << 20)  # never dereferenced
+
+
+# ---- the oracle -------------------------------------------------------------
+def test_oracle_rotation_keeps_relative_positions():
+    """q(p).k(r) depends on p - r alone, pairs keep their length, and the inverse undoes it."""
+    rng = np.random.default_rng(0)
+    f = 10000.0 ** (-np.arange(0, 32, 2) / 32)
+    for inter in (False, True):
+        q, k = rng.standard_normal((2, 64))
+        dots = [CO.rotate_row(q, p + 7, f, inter) @ CO.rotate_row(k, p, f, inter) for p in (0, 1, 50, 4000)]
+        assert np.allclose(dots, dots[0], atol=1e-9)
+        assert np.isclose(np.linalg.norm(CO.rotate_row(q, 99, f, inter)), np.linalg.norm(q))
+        assert np.allclose(CO.rotate_row(CO.rotate_row(q, 99, f, inter), 99, f, inter, inverse=True), q)
+    assert np.allclose(CO.rotate_row([1.0] + [0.0] * 63, 1, [np.pi / 2], False)[:2], [0, 1])
+    assert np.array_equal(CO.rotate_row(np.ones(64), 5, f)[32:], np.ones(32))
+
+
+def test_oracle_dense_decode_is_the_last_row_of_dense_attention():
+    """Against the prefill oracle with exact masses and every chunk (dense causal attention)."""
+    rng = np.random.default_rng(1)
+    n, d = 150, 64
+    q, k, v = rng.standard_normal((3, n, d))
+    t = lambda x: torch.from_numpy(x).view(1, 1, -1, d)
+    ref = O.forward(t(q), t(k), t(v), torch.zeros(1, 1, n // 64, d, dtype=torch.float64), 64, 2, mode="exact")
+    pages = np.zeros((4, 1, 64, d))
+    vpages = np.zeros((4, 1, 64, d))
+    for c, p in enumerate((2, 0, 3)):
+        m = min(64, n - 64 * c)
+        pages[p, 0, :m], vpages[p, 0, :m] = k[64 * c:64 * c + m], v[64 * c:64 * c + m]
+    out, lse, _, _ = CO.decode_dense(q[-1].reshape(1, 1, d), pages, vpages, [[2, 0, 3]], [n], d ** -0.5)
+    assert np.allclose(out[0, 0], ref["out"][0, 0, -1], atol=1e-12)
+    assert np.isclose(lse[0, 0], ref["lse"][0, 0, -1])
+
+
+# ---- the binding's checks ---------------------------------------------------
+B, H, G, N, D = 2, 8, 2, 70, 64
+
+
+def test_rotate_arguments():
+    q, k = torch.zeros(B, H, N, D, dtype=BF), torch.zeros(B, G, N, D, dtype=BF)
+    f = torch.ones(16)
+    assert check_rotate_args(q, f, k) == 0
+    assert check_rotate_args(q, f, k, torch.zeros(N, dtype=torch.int32)) == 0
+    assert check_rotate_args(q, f, k, torch.zeros(B, N, dtype=torch.int32)) == N
+    check_rotate_args(q, f, k, q_out=q, k_out=k)  # in place
+    check_rotate_args(q, f, k, q_out=torch.zeros(B, H, N, D), k_out=torch.zeros(B, G, N, D))
+    fused = torch.zeros(B, N, H + 2 * G, D, dtype=BF)
+    check_rotate_args(fused[:, :, :H].transpose(1, 2), f, fused[:, :, H:H + G].transpose(1, 2))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(k=torch.zeros(B, G, N - 1, D, dtype=BF)),
+    dict(k=torch.zeros(B, G, N, D)),
+    dict(k=torch.zeros(G, N, D, dtype=BF)),
+    dict(positions=torch.zeros(N, dtype=torch.int64)),
+    dict(positions=torch.zeros(N + 1, dtype=torch.int32)),
+    dict(positions=torch.zeros(1, N, dtype=torch.int32)),
+    dict(positions=torch.zeros(2 * N, dtype=torch.int32)[::2]),
+    dict(q_out=torch.zeros(B, H, N, D, dtype=torch.float16)),
+    dict(q_out=torch.zeros(B, H, N + 1, D, dtype=BF)),
+    dict(q_out=torch.zeros(B, N, H, D, dtype=BF).transpose(1, 2)),
+    dict(k_out=torch.zeros(B, G, N, D, dtype=BF)),
+    dict(inv_freq=None),
+])
+def test_rotate_refuses(kw):
+    a = dict(q=torch.zeros(B, H, N, D, dtype=BF), inv_freq=torch.ones(16))
+    a.update(kw)
+    with pytest.raises((ValueError, TypeError)):
+        check_rotate_args(**a)
+
+
+def test_rotate_refuses_overlapping_and_expanded_outputs():
+    f = torch.ones(16)
+    buf = torch.zeros(2 * B * H * N * D, dtype=BF)
+    q = buf[:B * H * N * D].view(B, H, N, D)
+    with pytest.raises(ValueError):  # shifted by one row
+        check_rotate_args(q, f, q_out=buf[D:D + B * H * N * D].view(B, H, N, D))
+    with pytest.raises(ValueError):  # one memory for every head, in place
+        x = torch.zeros(B, 1, N, D, dtype=BF).expand(B, H, N, D)
+        check_rotate_args(x, f, q_out=x)
+    k = torch.zeros(B, G, N, D, dtype=BF)
+    with pytest.raises(ValueError):  # k_out on q
+        check_rotate_args(q, f, k, k_out=q.view(-1)[:B * G * N * D].view(B, G, N, D))
+    with pytest.raises(ValueError):  # q_out on k
+        kk = buf[:B * G * N * D].view(B, G, N, D)
+        check_rotate_args(torch.zeros(B, H, N, D, dtype=BF), f, kk, q_out=q)
+
+
+@pytest.mark.parametrize("f", [torch.ones(0), torch.ones(4), torch.ones(40), torch.ones(16, dtype=torch.float64),
+                               torch.ones(4, 4), torch.ones(32)[::2]])
+def test_rope_refuses(f):
+    with pytest.raises((ValueError, TypeError)):
+        _abi._rope(f, False, 64)
+
+
+def test_rows_need_aligned_contiguous_rows():
+    x = torch.zeros(2, 3, 5, 72, dtype=BF)
+    assert _abi._rows(x[..., :64], "x").token_stride == 72
+    with pytest.raises(ValueError):
+        _abi._rows(x[..., 4:68], "x")
+    with pytest.raises(ValueError):
+        _abi._rows(torch.zeros(2, 3, 5, 68, dtype=BF)[..., :64], "x")
+    with pytest.raises(ValueError):
+        _abi._rows(torch.zeros(2, 3, 64, 8, dtype=BF).transpose(2, 3), "x")
+    # the stride of a single entry is not looked at
+    assert _abi._rows(torch.zeros(1, 3, 1, 64, dtype=BF).as_strided((1, 3, 1, 64), (7, 64, 5, 1)), "x").batch_stride == 0
+
+
+def _append_args(dtype=BF, **kw):
+    z = lambda *s: torch.zeros(*s, dtype=dtype)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    a = dict(k=z(9, G, D), v=z(9, G, D), k_pages=z(5, G, 64, D), v_pages=z(5, G, 64, D), block_table=i(B, 3),
+             max_chunks=3, seq_lens=i(B), q=z(9, H, D), cu_new=i(B + 1), full_pages=i(B + 9 // 64))
+    a.update(kw)
+    return a
+
+
+def test_append_arguments():
+    sh = make_shape(B, H, G, D, 3 * 64, 0, HILS_BF16)
+    z = lambda *s: torch.zeros(*s, dtype=BF)
+    check_append_args(sh, **_append_args(q_out=z(9, H, D)))
+    check_append_args(sh, **_append_args(k=z(B, G, D), v=z(B, G, D), q=z(B, H, D), cu_new=None))
+    check_append_args(sh, **_append_args(k=z(B, G, 40, D), v=z(B, G, 40, D), q=z(B, H, 40, D), cu_new=None,
+                                         new_lens=torch.zeros(B, dtype=torch.int32),
+                                         full_pages=torch.zeros(B + 80 // 64, dtype=torch.int32)))
+    check_append_args(make_shape(B, H, G, D, 3 * 64, 0, HILS_F32), **_append_args(torch.float32))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(k=torch.zeros(9, G, D)),
+    dict(v=torch.zeros(8, G, D, dtype=BF)),
+    dict(q=torch.zeros(9, G, D, dtype=BF)),
+    dict(cu_new=None),                                     # nine rows for two sequences
+    dict(cu_new=torch.zeros(B, dtype=torch.int32)),
+    dict(cu_new=torch.zeros(B + 1, dtype=torch.int64)),
+    dict(new_lens=torch.zeros(B, dtype=torch.int32)),      # packed rows have cu_new
+    dict(k=torch.zeros(B, G, 9, D, dtype=BF), v=torch.zeros(B, G, 9, D, dtype=BF), q=None),  # cu_new with padded rows
+    dict(k=torch.zeros(9, D, dtype=BF)),
+    dict(k_pages=torch.zeros(5, G, 32, D, dtype=BF)),
+    dict(v_pages=torch.zeros(4, G, 64, D, dtype=BF)),
+    dict(block_table=torch.zeros(B, 4, dtype=torch.int32)),
+    dict(block_table=torch.zeros(B, 3, dtype=torch.int64)),
+    dict(seq_lens=torch.zeros(B + 1, dtype=torch.int32)),
+    dict(full_pages=torch.zeros(B - 1, dtype=torch.int32)),
+    dict(q=None, q_out=torch.zeros(9, H, D, dtype=BF)),
+    dict(q_out=torch.zeros(9, H, D)),
+])
+def test_append_refuses(kw):
+    with pytest.raises((ValueError, TypeError)):
+        check_append_args(make_shape(B, H, G, D, 3 * 64, 0, HILS_BF16), **_append_args(**kw))
+
+
+def _dense_args(**kw):
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    a = dict(q=torch.zeros(B, H, D, dtype=BF), k_pages=torch.zeros(5, G, 64, D, dtype=BF),
+             v_pages=torch.zeros(5, G, 64, D, dtype=BF), block_table=i(B, 3), max_chunks=3, seq_lens=i(B))
+    a.update(kw)
+    return a
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=torch.zeros(B, H, D)), dict(q=torch.zeros(B, G, D, dtype=BF)),
+    dict(k_pages=torch.zeros(5, H, 64, D, dtype=BF)), dict(v_pages=torch.zeros(5, G, 64, D)),
+    dict(k_pages=torch.zeros(5, G, D, dtype=BF)), dict(block_table=torch.zeros(B, 2, dtype=torch.int32)),
+    dict(seq_lens=torch.zeros(B, dtype=torch.int64)), dict(out=torch.zeros(B, H, D)),
+    dict(lse=torch.zeros(B, H, dtype=BF)), dict(lse=torch.zeros(B, H, 1)),
+])
+def test_dense_refuses(kw):
+    sh = make_shape(B, H, G, D, 3 * 64, 0, HILS_BF16)
+    check_dense_args(sh, **_dense_args())
+    with pytest.raises((ValueError, TypeError)):
+        check_dense_args(sh, **_dense_args(**kw))
+
+
+def test_cache_calls_refuse_cpu_tensors_and_lengths_beyond_int32():
+    with pytest.raises(ValueError):
+        hils.rotate(torch.zeros(1, 1, 4, 64), torch.ones(32))
+    with pytest.raises(ValueError):
+        hils.decode_dense(torch.zeros(1, 1, 64), torch.zeros(1, 1, 64, 64), torch.zeros(1, 1, 64, 64),
+                          torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        hils.DenseDecode(1, 1, 1, 64, 1 << 25, "bf16")
+    with pytest.raises(ValueError):
+        hils.Append(1, 1, 1, 64, 1 << 25, "bf16")
+
+
+# ---- the C ABI's checks -----------------------------------------------------
+def _sh(**kw):
+    a = dict(batch=2, heads_q=8, heads_kv=2, head_dim=64, seq_len=640, top_k=0, dtype=1)
+    a.update(kw)
+    return make_shape(a["batch"], a["heads_q"], a["heads_kv"], a["head_dim"], a["seq_len"], a["top_k"], a["dtype"],
+                      window=a.get("window", 0))
+
+
+def test_rotate_rejects_before_launch():
+    L, ref = hils.lib(), ctypes.byref
+    s, r, ro = _sh(), Rows(1 << 20, 64, 64, 64), Rope(1 << 20, 32, 0)
+
+    def call(s=s, q=r, k=r, rope=ro, ps=0, qo=r, ko=r, od=1):
+        return L.hils_rotate(ref(s), q and ref(q), k and ref(k), rope and ref(rope), None, ps, 0, qo and ref(qo),
+                             ko and ref(ko), od, None)
+
+    assert call(q=None) == 1 and call(rope=None) == 1 and call(ko=None) == 1 and call(k=None) == 1
+    assert call(od=7) == 1 and call(ps=-1) == 1
+    assert call(q=Rows((1 << 20) + 8, 64, 64, 64)) == 1
+    assert call(qo=Rows(1 << 20, 64, 64, 60)) == 1
+    assert call(rope=Rope(None, 32, 0)) == 1 and call(rope=Rope(1 << 20, 80, 0)) == 1
+    assert call(rope=Rope(1 << 20, 0, 0)) == 1 and call(rope=Rope(1 << 20, 32, 2)) == 1
+    assert call(rope=Rope(1 << 20, 24, 0)) == 2
+    assert call(s=_sh(head_dim=96)) == 2
+    assert call(s=_sh(batch=0), q=None, qo=None) == 0 and call(s=_sh(seq_len=0)) == 0
+
+
+def test_append_rejects_before_launch():
+    L, ref = hils.lib(), ctypes.byref
+    s, r, ro = _sh(), Rows(1 << 20, 64, 64, 64), Rope(1 << 20, 32, 0)
+
+    def call(s=s, k=r, v=r, q=r, qo=r, n=4, cu=None, nl=None, sl=FAKE, bt=FAKE, mc=4, np_=4, rope=ro, kp=FAKE,
+             vp=FAKE, fp=None, ws=FAKE, wsb=256):
+        return L.hils_append_paged(ref(s), k and ref(k), v and ref(v), q and ref(q), qo and ref(qo), n, cu, nl, sl, bt,
+                                   mc, np_, rope and ref(rope), kp, vp, fp, ws, wsb, None)
+
+    assert call(k=None) == 1 and call(v=None) == 1 and call(q=None) == 1 and call(qo=None) == 1
+    assert call(n=-1) == 1 and call(cu=FAKE, nl=FAKE) == 1 and call(sl=None) == 1 and call(bt=None) == 1
+    assert call(mc=0) == 1 and call(np_=0) == 1 and call(kp=None) == 1 and call(vp=P_((1 << 20) + 4)) == 1
+    assert call(k=Rows(1 << 20, 64, 4, 64)) == 1
+    assert call(rope=Rope(1 << 20, 24, 0)) == 2 and call(mc=1 << 26) == 2
+    assert call(n=(1 << 31) - 1) == 2  # more rows than 32 bits count
+    assert call(ws=None) == 3 and call(wsb=128) == 3
+    assert call(s=_sh(batch=0)) == 0 and call(n=0, k=None, v=None, q=None, qo=None, ws=None) == 0
+    n = ctypes.c_size_t(0)
+    assert L.hils_workspace_size(ref(s), hils.OP_APPEND, ref(n)) == 0 and n.value >= 256
+
+
+def test_dense_rejects_before_launch():
+    L, ref = hils.lib(), ctypes.byref
+    s = _sh()
+    n = ctypes.c_size_t(0)
+    assert L.hils_workspace_size(ref(s), hils.OP_DECODE_DENSE, ref(n)) == 0 and n.value >= 256
+    size = n.value
+
+    def call(s=s, q=FAKE, k=FAKE, v=FAKE, bt=FAKE, mc=10, sl=FAKE, np_=4, out=FAKE, ws=FAKE, wsb=size):
+        return L.hils_decode_dense(ref(s), q, k, v, bt, mc, sl, np_, out, None, ws, wsb, None)
+
+    for name in ("q", "k", "v", "bt", "sl", "out"):
+        assert call(**{name: None}) == 1, name
+    assert call(mc=0) == 1 and call(mc=11) == 1 and call(np_=0) == 1
+    assert call(q=P_((1 << 20) + 8)) == 1
+    assert call(ws=None) == 3 and call(wsb=size - 1) == 3 and call(ws=P_((1 << 20) + 8)) == 3
+    assert call(s=_sh(heads_q=6)) == 2 and call(s=_sh(window=100)) == 1
+    assert call(s=_sh(batch=0)) == 0

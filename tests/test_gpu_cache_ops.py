@@ -1,0 +1,589 @@
+"""The paged-cache operators on the GPU against their fp64 oracle.
+
+Tolerances, derived from the arithmetic (u(t) = eps(t) / 2, half a step of the output type):
+* rotate: the output is x cos - y sin in fp32, rounded once.  The angle's remainder is rounded
+  to fp32 once (pi * 2^-24 at most), sincospif is good to 2 ulp of 1, the products and the sum
+  round three times: the value is off by at most (|x| + |y|) 2^-20, then u(out) relative.
+* dense: fp32 sums of d products are off by d 2^-23 sum |q||k| scale =: e_s (2^-23: a tensor
+  core may truncate); exp and the split of p into two bf16 parts add 2^-16 relative; the sums
+  over n keys n 2^-24.  So each p is off by r = 2 e_s + 2^-16 + n 2^-23 relative (twice e_s:
+  the logit and the normaliser), the output by r sum_j p_j |v_j| + u(out) |out|, the
+  log-sum-exp by r + 2^-22 |lse|.
+"""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import chunk_wise_hierarchical_b200 as hils
+from oracle import cache_oracle as CO
+from oracle import hils_oracle as O
+from parity_util import check_close
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _u(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def _randn(*shape, dtype, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
+def _freq(r):
+    return (10000.0 ** (-torch.arange(0, r, 2, dtype=torch.float64) / r)).float().cuda()
+
+
+def _close(got, want, bound, what=""):
+    got = _np(got) if torch.is_tensor(got) else got
+    assert got.shape == want.shape
+    assert np.array_equal(np.isfinite(got), np.isfinite(want)), what + ": finite values elsewhere"
+    fin = np.isfinite(want)
+    err = np.abs(got - np.where(fin, want, 0))[fin]
+    over = err - np.broadcast_to(bound, want.shape)[fin]
+    assert err.size == 0 or over.max() <= 0, f"{what}: off by {err[over.argmax()]:.3g}, {over.max():.3g} over its bound"
+
+
+# ---- rotate -----------------------------------------------------------------
+def _rotate_bound(x, want, out_dtype, rot, interleaved):
+    a = np.abs(x)
+    mag = np.zeros_like(a)
+    if interleaved:
+        pair = a[..., 0:rot:2] + a[..., 1:rot:2]
+        mag[..., 0:rot:2] = mag[..., 1:rot:2] = pair
+    else:
+        pair = a[..., :rot // 2] + a[..., rot // 2:rot]
+        mag[..., :rot // 2] = mag[..., rot // 2:rot] = pair
+    e = mag * 2.0 ** -20
+    return e + _u(out_dtype) * (np.abs(want) + e)
+
+
+@pytest.mark.parametrize("dtype,out_dtype", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("d,rot,inter", [(64, 64, False), (64, 16, True), (128, 128, True), (128, 96, False)])
+@pytest.mark.parametrize("b,h,g,n,pos", [(1, 1, 1, 1, None), (2, 8, 2, 37, "row"), (3, 4, 4, 65, "shared")])
+def test_rotate_matches_oracle(dtype, out_dtype, d, rot, inter, b, h, g, n, pos):
+    dt, od = DT[dtype], DT[out_dtype]
+    fused = _randn(b, n, h + 2 * g, d, dtype=dt, seed=b + d)
+    q, k = fused[:, :, :h].transpose(1, 2), fused[:, :, h:h + g].transpose(1, 2)
+    p = None
+    if pos:  # far positions, the largest int32 and negative ones among them
+        gen = torch.Generator().manual_seed(5)
+        p = torch.randint(0, 1 << 23, (n,) if pos == "shared" else (b, n), generator=gen, dtype=torch.int32)
+        p.view(-1)[0], p.view(-1)[-1] = 2**31 - 1, -12345
+    f = _freq(rot)
+    for inverse in (False, True):
+        qo = torch.full((b, h, n, d), 7.0, dtype=od, device="cuda")
+        ko = torch.full((b, g, n, d), 7.0, dtype=od, device="cuda")
+        hils.rotate(q, f, k=k, positions=None if p is None else p.cuda(), inverse=inverse, interleaved=inter,
+                    q_out=qo, k_out=ko)
+        for x, o in ((q, qo), (k, ko)):
+            want = CO.rotate(_np(x), _np(f), None if p is None else p.numpy(), inter, inverse)
+            _close(o, want, _rotate_bound(_np(x), want, od, rot, inter), "rotate")
+
+
+def test_rotate_in_place_and_alone():
+    q = _randn(2, 4, 130, 64, dtype=torch.bfloat16, seed=0)
+    f = _freq(64)
+    want = hils.rotate(q, f)
+    assert torch.equal(hils.rotate(q.clone(), f, q_out=None), want)
+    x = q.clone()
+    assert hils.rotate(x, f, q_out=x) is x and torch.equal(x, want)
+    # a slice of a fused projection, in place: the other slices stay
+    fused = _randn(2, 130, 12, 64, dtype=torch.bfloat16, seed=1)
+    ref = fused.clone()
+    s = fused[:, :, :4].transpose(1, 2)
+    r = hils.rotate(s, f)
+    hils.rotate(s, f, q_out=s)
+    assert torch.equal(s, r) and torch.equal(fused[:, :, 4:], ref[:, :, 4:])
+    assert hils.rotate(q[:, :, :0], f).shape == (2, 4, 0, 64)
+    assert hils.rotate(q[:0], f).shape == (0, 4, 130, 64)
+
+
+def test_rotate_inverse_is_the_gradient():
+    """L = sum(y * rotate(x)) is linear in x: its gradient is rotate^-1(y), checked against the
+    formula and against differences of the oracle's L."""
+    b, h, n, d, rot = 1, 2, 9, 64, 32
+    x, y = _randn(b, h, n, d, dtype=torch.float32, seed=3), _randn(b, h, n, d, dtype=torch.float32, seed=4)
+    f = _freq(rot)
+    for inter in (False, True):
+        grad = _np(hils.rotate(y, f, inverse=True, interleaved=inter))
+        rng = np.random.default_rng(0)
+        for _ in range(12):
+            at = tuple(rng.integers(0, s) for s in x.shape)
+            step = np.zeros(x.shape)
+            step[at] = 0.5
+            lo, hi = (np.sum(_np(y) * CO.rotate(_np(x) + s * step, _np(f), None, inter)) for s in (-1, 1))
+            assert abs((hi - lo) - grad[at]) <= 8 * 2.0 ** -20
+        # and it undoes the rotation: two roundings of the same bound
+        back = hils.rotate(hils.rotate(x, f, interleaved=inter), f, inverse=True, interleaved=inter)
+        _close(back, _np(x), 3 * _rotate_bound(_np(x), _np(x), torch.float32, rot, inter) + 2.0 ** -19, "round trip")
+
+
+# ---- append -----------------------------------------------------------------
+def _table(lens, max_chunks, pool, seed):
+    perm = np.random.RandomState(seed).permutation(pool)
+    t = np.full((len(lens), max_chunks), -1, np.int32)
+    at = 0
+    for b, n in enumerate(lens):
+        c = -(-n // 64)
+        t[b, :c] = perm[at:at + c]
+        at += c
+    assert at <= pool
+    return t
+
+
+def _append_check(layout, counts, lens, h, g, d, dtype, rot, inter, with_q=True, pad_rows=0, spoil=None):
+    dt = DT[dtype]
+    b = len(counts)
+    max_chunks = max(1, -(-max(lens) // 64))
+    pool = sum(-(-n // 64) for n in lens) + 2
+    table = _table(lens, max_chunks, pool, seed=1)
+    if spoil:
+        spoil(table)
+    kp, vp = _randn(pool, g, 64, d, dtype=dt, seed=2), _randn(pool, g, 64, d, dtype=dt, seed=3)
+    kp0, vp0 = kp.clone(), vp.clone()
+    f = _freq(rot) if rot else None
+    call = hils.Append(b, h, g, d, max_chunks, dt, inv_freq=f, interleaved=inter)
+    kw = {}
+    if layout == "packed":
+        cu = np.concatenate([[0], np.cumsum(counts)])
+        t = int(cu[-1]) + pad_rows
+        fused = _randn(t, h + 2 * g, d, dtype=dt, seed=4)
+        q, k, v = fused[:, :h], fused[:, h:h + g], fused[:, h + g:]
+        kw["cu_new"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        row = lambda x, bi, i: _np(x[int(cu[bi]) + i])
+        at = lambda bi, i: int(cu[bi]) + i
+        start = lambda bi: int(cu[bi])
+        tokens = t
+    elif layout == "single":
+        assert all(c == 1 for c in counts)
+        fused = _randn(b, h + 2 * g, d, dtype=dt, seed=4)
+        q, k, v = fused[:, :h], fused[:, h:h + g], fused[:, h + g:]
+        row = lambda x, bi, i: _np(x[bi])
+        at = lambda bi, i: bi
+        start = lambda bi: bi
+        tokens = b
+    else:
+        n = max(counts) + pad_rows
+        q, k, v = (_randn(b, x, n, d, dtype=dt, seed=4 + x) for x in (h, g, g + 100))
+        v = v[:, :g]  # strides of its own
+        if min(counts) < n:
+            kw["new_lens"] = torch.tensor(counts, dtype=torch.int32, device="cuda")
+        row = lambda x, bi, i: _np(x[bi, :, i])
+        at = lambda bi, i: (bi, slice(None), i)
+        start = lambda bi: bi * n
+        tokens = b * n
+    q_out = torch.full(q.shape, 7.0, dtype=dt, device="cuda") if with_q else None
+    full = torch.full((hils.append_slots(b, tokens),), 99, dtype=torch.int32, device="cuda")
+    call(k, v, kp, vp, torch.from_numpy(table).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"),
+         q=q if with_q else None, q_out=q_out, full_pages=full, **kw)
+    status = call.device_status()
+    q_rows, wk, wv, filled = CO.append(
+        lambda bi, i: (row(q, bi, i) if with_q else None, row(k, bi, i), row(v, bi, i)),
+        _np(kp0), _np(vp0), table, lens, counts, None if f is None else _np(f), inter)
+    assert torch.equal(vp, torch.from_numpy(wv).to(dt).cuda()), "values are copied"
+    keys = np.abs(_np(kp0)).max()
+    changed = np.abs(wk - _np(kp0)) > 0
+    assert np.array_equal(_np(kp)[~changed], _np(kp0)[~changed]), "untouched rows stay"
+    mag = max(keys, np.abs(_np(k)).max() if k.numel() else 0)
+    _close(kp, wk, np.where(changed, 2 * mag * 2.0 ** -20 * (1 + _u(dt)) + _u(dt) * np.abs(wk), 0), "k_pages")
+    if with_q:
+        got = _np(q_out)
+        want = np.full(got.shape, 7.0)
+        for (bi, i), x in q_rows.items():
+            want[at(bi, i)] = x
+        qm = np.abs(_np(q)).max() if q.numel() else 0
+        _close(got, want, np.where(want == 7.0, 0, 2 * qm * 2.0 ** -20 * 2 + _u(dt) * np.abs(want)), "q_out")
+    got = full.cpu().numpy()
+    want = np.full(got.shape, -1)
+    for bi, pages in enumerate(filled):
+        s0 = bi + start(bi) // 64
+        want[s0:s0 + len(pages)] = pages
+    assert np.array_equal(got, want), "full_pages"
+    return status
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,h,g,rot,inter", [(64, 2, 2, 64, False), (128, 8, 2, 128, False), (128, 8, 1, 32, True),
+                                             (64, 4, 1, 0, False)])
+@pytest.mark.parametrize("layout,counts,lens", [
+    ("single", [1, 1, 1, 1], [1, 64, 65, 1000]),
+    ("packed", [1], [1]),
+    ("packed", [64, 0, 130, 1, 0, 63], [64, 10, 200, 128, 0, 127]),
+    ("padded", [70, 0, 33], [70, 5, 161]),
+    ("padded", [5, 5], [5, 69]),
+])
+def test_append_matches_oracle(dtype, d, h, g, rot, inter, layout, counts, lens):
+    assert _append_check(layout, counts, lens, h, g, d, dtype, rot, inter) == 0
+
+
+def test_append_without_queries_and_with_padding_rows():
+    assert _append_check("packed", [3, 70], [3, 70], 2, 2, 64, "bf16", 64, False, with_q=False, pad_rows=9) == 0
+    assert _append_check("packed", [3, 70], [3, 70], 2, 2, 64, "bf16", 64, False, pad_rows=100) == 0
+    assert _append_check("padded", [3, 70], [3, 70], 2, 2, 64, "bf16", 64, False, pad_rows=30) == 0
+    assert _append_check("packed", [0, 0], [3, 0], 2, 2, 64, "f32", 64, False) == 0
+
+
+def test_append_of_many_sequences():
+    """More sequences than one CTA has threads, most of them without new tokens."""
+    rng = np.random.RandomState(0)
+    counts = [int(rng.randint(1, 80)) if i % 7 == 0 else 0 for i in range(700)]
+    lens = [c + int(rng.randint(0, 70)) for c in counts]
+    assert _append_check("packed", counts, lens, 1, 1, 64, "bf16", 64, False) == 0
+
+
+def test_append_skips_and_flags_bad_pages():
+    def spoil(t):
+        t[0, 1] = -1
+        t[1, 0] = 1 << 30
+    assert _append_check("packed", [100, 5], [130, 20], 2, 2, 64, "bf16", 64, False, spoil=spoil) == 5
+    # more new tokens than the length holds: positions below zero
+    dev = "cuda"
+    call = hils.Append(1, 1, 1, 64, 1, "f32", inv_freq=_freq(64))
+    kp = torch.zeros(1, 1, 64, 64, device=dev)
+    k = torch.ones(4, 1, 64, device=dev)
+    q_out = torch.full((4, 1, 64), 7.0, device=dev)
+    i = lambda *x: torch.tensor(x, dtype=torch.int32, device=dev)
+    full = torch.empty(1, dtype=torch.int32, device=dev)
+    call(k, k, kp, kp.clone(), i(0).view(1, 1), i(1), q=k, q_out=q_out, cu_new=i(0, 4), full_pages=full)
+    assert call.device_status() == 5 and call.device_status() == 0
+    assert (q_out[:3] == 7).all() and torch.equal(q_out[3], k[3]) and kp[0, 0, 1:].abs().max() == 0
+    assert torch.equal(kp[0, 0, 0], k[0, 0]) and full.item() == -1
+    # beyond the table: queries are rotated, nothing is written
+    kp.zero_()
+    call(k, k, kp, kp.clone(), i(0).view(1, 1), i(66), q=k, q_out=q_out, cu_new=i(0, 4))
+    assert call.device_status() == 5
+    want = CO.rotate(np.ones((1, 1, 4, 64)), _np(_freq(64)), [62, 63, 64, 65])[0, 0]
+    _close(q_out[:, 0], want, 2.0 ** -18, "q")
+    assert kp[0, 0, :62].abs().max() == 0 and kp[0, 0, 62:].abs().min() > 0
+
+
+# ---- dense decode -----------------------------------------------------------
+def _dense_case(lens, h, g, d, dtype, window=0, scale=None, seed=0, needles=True, garbage=False, spare=2):
+    dt = DT[dtype]
+    b = len(lens)
+    max_chunks = max(1, -(-max(lens) // 64))
+    pool = sum(-(-max(n, 0) // 64) for n in lens) + spare
+    table = _table([max(n, 0) for n in lens], max_chunks, pool, seed)
+    q = _randn(b, h, d, dtype=dt, seed=seed)
+    kp, vp = _randn(pool, g, 64, d, dtype=dt, seed=seed + 1), _randn(pool, g, 64, d, dtype=dt, seed=seed + 2)
+    if needles:
+        for bi, n in enumerate(lens):
+            if n > 0:
+                j = (n * 7) // 11
+                kp[table[bi, j // 64], :, j % 64] = (8 * q[bi, 0].float() / q[bi, 0].float().norm()).to(dt)
+    if garbage:  # what lies behind the last token of each sequence, and in pages of none
+        used = np.zeros((pool, 64), bool)
+        for bi, n in enumerate(lens):
+            for j in range(n):
+                used[table[bi, j // 64], j % 64] = True
+        free = torch.from_numpy(~used).cuda()
+        for x, bad in ((kp, math.nan), (vp, math.inf)):
+            x.transpose(1, 2)[free] = bad
+    return dict(q=q, k_pages=kp, v_pages=vp, block_table=torch.from_numpy(table).cuda(),
+                seq_lens=torch.tensor(lens, dtype=torch.int32, device="cuda")), (window, scale)
+
+
+def _dense_want(t, window, scale):
+    d = t["q"].shape[-1]
+    return CO.decode_dense(_np(t["q"]), _np(t["k_pages"]), _np(t["v_pages"]), t["block_table"].cpu().numpy(),
+                           t["seq_lens"].cpu().numpy(), scale if scale is not None else d ** -0.5, window)
+
+
+def _dense_close(out, lse, t, window, scale):
+    want, wlse, mag, size = _dense_want(t, window, scale)
+    d, n = t["q"].shape[-1], max(1, int(t["seq_lens"].max()))
+    r = 2 * d * 2.0 ** -23 * size + 2.0 ** -16 + n * 2.0 ** -23
+    _close(out, want, r[..., None] * mag + _u(out.dtype) * (np.abs(want) + r[..., None] * mag), "out")
+    _close(lse, wlse, r + 2.0 ** -22 * np.abs(np.where(np.isfinite(wlse), wlse, 0)), "lse")
+
+
+def _dense_run(t, window=0, scale=None):
+    b, h, d = t["q"].shape
+    call = hils.DenseDecode(b, h, t["k_pages"].shape[1], d, t["block_table"].shape[1], t["q"].dtype, window=window,
+                            scale=scale)
+    lse = torch.full((b, h), 5.0, device="cuda")
+    out = call(**t, lse=lse)
+    assert call.device_status() == 0
+    return out, lse
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("h,g", [(2, 2), (4, 2), (8, 2), (16, 2), (8, 1)])
+def test_dense_matches_oracle(dtype, d, h, g):
+    t, w = _dense_case([1, 0, 64, 65, 1000, 63, 127, 16, 17, 33], h, g, d, dtype, seed=h + d, garbage=False)
+    _dense_close(*_dense_run(t), t, *w)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,h,g,d", [([4500], 4, 1, 64), ([1], 1, 1, 64), ([0], 8, 1, 128), ([3001, 2], 2, 2, 128)])
+def test_dense_few_sequences(dtype, lens, h, g, d):
+    t, w = _dense_case(lens, h, g, d, dtype, seed=3)
+    _dense_close(*_dense_run(t), t, *w)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [64, 128, 512])
+def test_dense_window(dtype, window):
+    t, _ = _dense_case([1, 64, 65, 700, 0, 512, 513, 129], 4, 2, 64, dtype, seed=window)
+    _dense_close(*_dense_run(t, window=window), t, window, None)
+
+
+@pytest.mark.parametrize("scale", [0.5, -0.25, 3.0])
+def test_dense_scale(scale):
+    t, _ = _dense_case([300, 31], 4, 2, 64, "f32", seed=9)
+    _dense_close(*_dense_run(t, scale=scale), t, 0, scale)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[5, 64, 0, 193, 1], [2000]])
+def test_dense_looks_at_nothing_behind_the_last_token(dtype, lens):
+    t, w = _dense_case(lens, 8, 2, 64, dtype, seed=5, garbage=True)
+    clean = {k: v.clone() for k, v in t.items()}
+    for x in (clean["k_pages"], clean["v_pages"]):
+        x.nan_to_num_(0.0, 0.0, 0.0)
+    out, lse = _dense_run(t)
+    _dense_close(out, lse, clean, *w)
+
+
+def test_dense_infinite_and_missing_logits():
+    """A key of -inf gets no weight; a row whose every logit is -inf is zero; NaN stays NaN."""
+    for dtype in ("bf16", "f32"):
+        t, w = _dense_case([200, 200, 200, 90], 2, 2, 64, dtype, seed=6, needles=False)
+        t["q"] = t["q"].abs() + 0.5
+        kp, vp, bt = t["k_pages"], t["v_pages"], t["block_table"].cpu().numpy()
+        kp[bt[0, 1], :, 5] = -math.inf          # one key
+        for c in range(4):
+            kp[bt[1, c]] = -math.inf            # every key of sequence 1
+        kp[bt[2, 0], :, 3] = math.nan
+        kp[bt[3, 0]] = -math.inf                # a whole page, the rest is fine
+        out, lse = _dense_run(t)
+        assert torch.isfinite(out[0]).all() and (out[1] == 0).all() and torch.isnan(out[2]).all()
+        assert (lse[1] == -math.inf).all()
+        kk = _np(kp)
+        ref = {**t, "k_pages": torch.from_numpy(np.where(np.isneginf(kk), -1e6, np.nan_to_num(kk, neginf=-1e6)))}
+        want, wlse, mag, _ = _dense_want({**ref, "k_pages": ref["k_pages"].cuda()}, *w)
+        for bi in (0, 3):
+            r = 2 * 64 * 2.0 ** -23 * 200 + 2.0 ** -15
+            _close(out[bi], want[bi], r * mag[bi] + 1.01 * _u(out.dtype) * np.abs(want[bi]) + 1e-9, "out")
+
+
+def test_dense_every_length_of_a_ragged_batch():
+    lens = list(range(0, 260)) + [1500, 3]
+    t, w = _dense_case(lens, 2, 1, 64, "bf16", seed=11)
+    _dense_close(*_dense_run(t), t, *w)
+
+
+def test_dense_shared_pages_and_the_same_sequence_twice():
+    t, w = _dense_case([640, 640, 100], 4, 2, 64, "bf16", seed=12)
+    t["block_table"][1] = t["block_table"][0]
+    t["q"][1] = t["q"][0]
+    out, lse = _dense_run(t)
+    _dense_close(out, lse, t, *w)
+
+
+def test_dense_skips_and_flags_bad_pages():
+    t, w = _dense_case([300, 300, 64], 4, 2, 64, "bf16", seed=13, needles=False)
+    t["block_table"][0, 2] = -1
+    t["block_table"][1, 0] = 1 << 30
+    t["block_table"][2, 0] = t["k_pages"].shape[0]
+    b, h, d = t["q"].shape
+    call = hils.DenseDecode(b, h, 2, d, t["block_table"].shape[1], t["q"].dtype)
+    lse = torch.empty(b, h, device="cuda")
+    out = call(**t, lse=lse)
+    assert call.device_status() == 5 and call.device_status() == 0
+    _dense_close(out, lse, t, *w)
+    assert (out[2] == 0).all()
+    # a length beyond the table: its keys are those the table has
+    t, w = _dense_case([300, 200], 4, 2, 64, "f32", seed=14)
+    t["seq_lens"][0] = 64 * t["block_table"].shape[1] + 7
+    call = hils.DenseDecode(2, 4, 2, 64, t["block_table"].shape[1], "f32")
+    out = call(**t)
+    assert call.device_status() == 5
+    t["seq_lens"][0] = 64 * t["block_table"].shape[1]
+    want = _dense_want(t, *w)[0]
+    assert np.abs(_np(out) - want).max() < 1e-4
+
+
+def test_dense_pool_beyond_32_bit_offsets():
+    """Pages whose element offsets pass 2^31 and 2^32."""
+    g, d, P = 8, 128, 68000  # 64 * 8 * 128 * 68000 = 4.46e9 elements, 8.9 GB each
+    kp = torch.empty(P, g, 64, d, dtype=torch.bfloat16, device="cuda")
+    vp = torch.empty_like(kp)
+    ids = [0, 33000, P - 1, 65537]
+    for n, p in enumerate(ids):
+        kp[p] = _randn(g, 64, d, dtype=torch.bfloat16, seed=n)
+        vp[p] = _randn(g, 64, d, dtype=torch.bfloat16, seed=n + 50)
+    q = _randn(1, g, d, dtype=torch.bfloat16, seed=99)
+    i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    # append the last 3 tokens there too
+    k, v = _randn(3, g, d, dtype=torch.bfloat16, seed=100), _randn(3, g, d, dtype=torch.bfloat16, seed=101)
+    hils.append_paged(k, v, kp, vp, i([ids]), i([250]), cu_new=i([0, 3]))
+    out, lse = hils.decode_dense(q, kp, vp, i([ids]), i([250]), return_lse=True)
+    small = dict(q=q, k_pages=kp[ids].clone(), v_pages=vp[ids].clone(), block_table=i([[0, 1, 2, 3]]), seq_lens=i([250]))
+    assert torch.equal(small["k_pages"][3, :, 55:58], k.transpose(0, 1))
+    _dense_close(out, lse, small, 0, None)
+
+
+def test_dense_lse_joins_windows():
+    """Two windows' outputs joined by their log masses give the whole."""
+    t, w = _dense_case([640], 4, 2, 64, "f32", seed=15)
+    out, lse = _dense_run(t)
+    a, la = _dense_run(t, window=128)
+    first = {**t, "seq_lens": t["seq_lens"] - 128}
+    c, lc = _dense_run(first)
+    z = torch.logaddexp(la, lc)
+    joined = a * (la - z).exp()[..., None] + c * (lc - z).exp()[..., None]
+    assert (z - lse).abs().max() < 2e-5 and (joined - out).abs().max() < 2e-5
+
+
+# ---- streams, graphs, repeats -----------------------------------------------
+def test_dense_repeats_bit_for_bit_and_on_another_stream():
+    t, w = _dense_case([5000, 0, 700, 33, 2500], 8, 2, 128, "bf16", seed=16)
+    out, lse = _dense_run(t)
+    for _ in range(5):
+        o, l = _dense_run(t)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    o, l = hils.decode_dense(**t, return_lse=True, stream=side)
+    side.synchronize()
+    assert torch.equal(o, out) and torch.equal(l, lse)
+    with torch.cuda.stream(side):
+        call = hils.DenseDecode(5, 8, 2, 128, t["block_table"].shape[1], torch.bfloat16)
+    torch.cuda.synchronize()
+    assert torch.equal(call(**t), out)
+
+
+def test_two_workspaces_at_once():
+    t, _ = _dense_case([3000, 700], 8, 2, 64, "bf16", seed=17)
+    u, _ = _dense_case([900, 2800], 8, 2, 64, "bf16", seed=18)
+    want = [_dense_run(x)[0] for x in (t, u)]
+    calls = [hils.DenseDecode(2, 8, 2, 64, x["block_table"].shape[1], torch.bfloat16) for x in (t, u)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(10):
+        for c, s, x, o in zip(calls, streams, (t, u), outs):
+            with torch.cuda.stream(s):
+                o.append(c(**x))
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w, y) for y in o)
+
+
+def test_a_decode_step_in_a_graph():
+    """rotate + append + summaries of the filled pages + both decodes, captured once and
+    replayed while the lengths grow on the device: each step against a fresh eager call."""
+    b, h, g, d, K = 2, 4, 2, 64, 3
+    dt = torch.bfloat16
+    max_chunks, pool = 5, 12
+    table = torch.from_numpy(_table([320, 320], max_chunks, pool, 3)).cuda()
+    kp, vp = torch.zeros(pool, g, 64, d, dtype=dt, device="cuda"), torch.zeros(pool, g, 64, d, dtype=dt, device="cuda")
+    lm = _randn(pool, h, d, dtype=dt, seed=1)
+    kbar, hb = torch.zeros(pool, h, d, device="cuda"), torch.zeros(pool, h, device="cuda")
+    lens = torch.tensor([60, 190], dtype=torch.int32, device="cuda")
+    f = _freq(64)
+    fused = torch.empty(b, h + 2 * g, d, dtype=dt, device="cuda")
+    app = hils.Append(b, h, g, d, max_chunks, dt, inv_freq=f)
+    dense = hils.DenseDecode(b, h, g, d, max_chunks, dt)
+    sparse = hils.Decode(b, h, g, d, max_chunks, K, dt)
+    q = torch.empty(b, h, d, dtype=dt, device="cuda")
+    full = torch.empty(hils.append_slots(b, b), dtype=torch.int32, device="cuda")
+    out_d, out_s, lse = torch.empty_like(q), torch.empty_like(q), torch.empty(b, h, device="cuda")
+    # the prompts
+    n0 = lens.tolist()
+    prompt = _randn(sum(n0), h + 2 * g, d, dtype=dt, seed=2)
+    cu = torch.tensor([0, n0[0], sum(n0)], dtype=torch.int32, device="cuda")
+    pf = torch.empty(hils.append_slots(b, sum(n0)), dtype=torch.int32, device="cuda")
+    app(prompt[:, h:h + g], prompt[:, h + g:], kp, vp, table, lens, cu_new=cu, full_pages=pf)
+    hils.summarize_paged(kp, lm, pf, kbar, hb)
+
+    def step():
+        lens.add_(1)
+        app(fused[:, h:h + g], fused[:, h + g:], kp, vp, table, lens, q=fused[:, :h], q_out=q, full_pages=full)
+        hils.summarize_paged(kp, lm, full, kbar, hb)
+        dense(q, kp, vp, table, lens, out=out_d, lse=lse)
+        sparse(q, kp, vp, kbar, hb, table, lens, out=out_s)
+
+    state = [x.clone() for x in (lens, kp, vp, kbar, hb)]
+    fused.copy_(_randn(b, h + 2 * g, d, dtype=dt, seed=99))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for x, y in zip((lens, kp, vp, kbar, hb), state):
+        x.copy_(y)
+    rows = [[prompt[:n0[0], h:]], [prompt[n0[0]:, h:]]]
+    for i in range(8):  # sequence 0 fills its first page at the fourth step, sequence 1 at the second
+        new = _randn(b, h + 2 * g, d, dtype=dt, seed=10 + i)
+        fused.copy_(new)
+        for bi in range(b):
+            rows[bi].append(new[bi:bi + 1, h:])
+        graph.replay()
+        torch.cuda.synchronize()
+        n = [x + i + 1 for x in n0]
+        assert lens.tolist() == n and app.device_status() == 0 and dense.device_status() == 0
+        want = hils.rotate(new[:, None, :h].transpose(1, 2), f,
+                           positions=torch.tensor([[x - 1] for x in n], dtype=torch.int32, device="cuda"))
+        assert torch.equal(q, want[:, :, 0])
+        _dense_close(out_d, lse, dict(q=q, k_pages=kp, v_pages=vp, block_table=table, seq_lens=lens), 0, None)
+        for bi in range(b):
+            # the pages hold the rotated rows, as rotating the whole sequence gives them
+            kv = torch.cat(rows[bi])
+            kr = hils.rotate(kv[None, :, :g].transpose(1, 2).contiguous(), f)[0]
+            for c in range(-(-n[bi] // 64)):
+                m = min(64, n[bi] - 64 * c)
+                p = int(table[bi, c])
+                assert torch.equal(kp[p, :, :m], kr[:, 64 * c:64 * c + m])
+                assert torch.equal(vp[p, :, :m].transpose(0, 1), kv[64 * c:64 * c + m, g:])
+        ref = O.decode(q.cpu(), kp.cpu(), vp.cpu(), lm.cpu(), table.cpu().numpy(), lens.cpu().numpy(), K)
+        check_close(out_s.float().cpu().numpy(), ref["out"], True)
+
+
+def test_prompt_through_the_framework():
+    """A prompt as a user runs it: rotated projections through attend, the same tokens appended
+    to the cache; the last row from the cache (K = all chunks, so both layers see every key)."""
+    b, h, g, n, d = 2, 4, 2, 190, 64
+    dt = torch.bfloat16
+    fused = _randn(b, n, h + 2 * g, d, dtype=dt, seed=30)
+    f = _freq(d)
+    sl = [fused[:, :, i:j].transpose(1, 2) for i, j in ((0, h), (h, h + g), (h + g, h + 2 * g))]
+    q, k = hils.rotate(sl[0], f, k=sl[1])
+    v = sl[2].contiguous()
+    lm = _randn(b, h, n // 64, d, dtype=dt, seed=31)
+    out, lse = hils.attend(q, k, v, lm, 4, return_lse=True)
+    table = torch.arange(6, dtype=torch.int32, device="cuda").view(2, 3)
+    kp, vp = torch.zeros(6, g, 64, d, dtype=dt, device="cuda"), torch.zeros(6, g, 64, d, dtype=dt, device="cuda")
+    lens = torch.full((b,), n, dtype=torch.int32, device="cuda")
+    full = torch.empty(hils.append_slots(b, b * n), dtype=torch.int32, device="cuda")
+    qa = hils.append_paged(sl[1], sl[2], kp, vp, table, lens, inv_freq=f, q=sl[0], full_pages=full)
+    assert torch.equal(qa, q)
+    assert sorted(x for x in full.tolist() if x >= 0) == [0, 1, 3, 4]
+    flat = kp.view(2, 3, g, 64, d).transpose(1, 2).reshape(b, g, 192, d)[:, :, :n]
+    assert torch.equal(flat, k)
+    lp = torch.zeros(6, h, d, dtype=dt, device="cuda")
+    lp.view(2, 3, h, d)[:, :2] = lm.transpose(1, 2)
+    kbar, hb = torch.zeros(6, h, d, device="cuda"), torch.zeros(6, h, device="cuda")
+    hils.summarize_paged(kp, lp, full, kbar, hb)
+    last = q[:, :, -1].contiguous()
+    sparse = hils.decode(last, kp, vp, kbar, hb, table, lens, 4)
+    assert (sparse.float() - out[:, :, -1].float()).abs().max() < 2e-2
+    dense, dl = hils.decode_dense(last, kp, vp, table, lens, return_lse=True)
+    _dense_close(dense, dl, dict(q=last, k_pages=kp, v_pages=vp, block_table=table, seq_lens=lens), 0, None)
