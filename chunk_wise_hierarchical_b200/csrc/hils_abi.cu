@@ -211,6 +211,9 @@ hils_status check_rope(const hils_rope* r, int head_dim) {
     return HILS_ERR_INVALID_ARG;
   return r->rotary_dim % 16 == 0 ? HILS_OK : HILS_ERR_UNSUPPORTED;
 }
+size_t dense_bytes(const hils_shape* s) {
+  return kHeader + align_up(hils::decode_dense_scratch(s->batch, s->heads_q, s->heads_kv, s->head_dim).total);
+}
 hils::Rows rows_of(const hils_rows* r) { return {r->data, r->batch_stride, r->head_stride, r->token_stride}; }
 size_t elem_size(int32_t dtype) { return dtype == HILS_BF16 ? 2 : 4; }
 
@@ -245,7 +248,7 @@ hils_status hils_workspace_size(const hils_shape* s, int32_t op, size_t* bytes) 
     case HILS_OP_DECODE: *bytes = decode_layout(s).total; return HILS_OK;
     case HILS_OP_ATTEND_SELECTED: *bytes = kHeader + cm_bytes(s); return HILS_OK;
     case HILS_OP_BACKWARD: *bytes = backward_layout(s).total; return HILS_OK;
-    case HILS_OP_DECODE_DENSE: *bytes = kHeader; return HILS_OK;
+    case HILS_OP_DECODE_DENSE: *bytes = dense_bytes(s); return HILS_OK;
     case HILS_OP_APPEND: *bytes = kHeader; return HILS_OK;
   }
   return HILS_ERR_INVALID_ARG;
@@ -553,14 +556,15 @@ hils_status hils_decode_dense(const hils_shape* s, const void* q, const void* k_
   if ((long long)max_chunks > ((long long)s->seq_len + s->chunk - 1) / s->chunk) return HILS_ERR_INVALID_ARG;
   if (!q || !k_pages || !v_pages || !block_table || !seq_lens || !out) return HILS_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out)) return HILS_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < kHeader || !aligned16(ws)) return HILS_ERR_WORKSPACE;
+  if (!hils::decode_dense_supported(s->heads_kv, max_chunks, n_pages)) return HILS_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < dense_bytes(s) || !aligned16(ws)) return HILS_ERR_WORKSPACE;
   hils::DenseArgs a{};
   a.q = q; a.k_pages = k_pages; a.v_pages = v_pages; a.block_table = block_table; a.seq_lens = seq_lens;
   a.out = out; a.lse = lse_out; a.err = static_cast<unsigned*>(ws);
   a.b = s->batch; a.h = s->heads_q; a.g = s->heads_kv; a.d = s->head_dim;
   a.max_chunks = max_chunks; a.n_pages = n_pages; a.n_win = s->window / s->chunk;
   a.scale = eff_scale(s); a.bf16 = s->dtype == HILS_BF16; a.poll = g_wait_limit.load();
-  return cuda_status(hils::run_decode_dense(a, (cudaStream_t)stream));
+  return cuda_status(hils::run_decode_dense(a, static_cast<char*>(ws) + kHeader, (cudaStream_t)stream));
 }
 
 hils_status hils_device_status(void* ws, void* stream) {

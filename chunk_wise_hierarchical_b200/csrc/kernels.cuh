@@ -262,6 +262,12 @@ struct DenseArgs {
   bool bf16;
   uint32_t poll;
 };
-cudaError_t run_decode_dense(DenseArgs a, cudaStream_t st);
+// Scratch of a dense decode: partials of the cut (sequence, KV head)s and their tickets.
+struct DenseScratch {
+  size_t part, part_ml, ticket, total;
+};
+DenseScratch decode_dense_scratch(int b, int h, int g, int d);
+bool decode_dense_supported(int g, int max_chunks, int n_pages);
+cudaError_t run_decode_dense(const DenseArgs& a, void* scratch, cudaStream_t st);
 
 }  // namespace hils

@@ -379,6 +379,38 @@ def test_dense_infinite_and_missing_logits():
             _close(out[bi], want[bi], r * mag[bi] + 1.01 * _u(out.dtype) * np.abs(want[bi]) + 1e-9, "out")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("h,g", [(2, 2), (4, 2), (8, 2), (16, 2)])
+def test_dense_long_caches(dtype, d, h, g):
+    """Enough keys that every stage of each SM's ring is filled several times, cut at odd
+    places; against the definition in 64 bits on the GPU."""
+    lens = [60001, 333, 0, 20000, 7777]
+    t, _ = _dense_case(lens, h, g, d, dtype, seed=h + d)
+    out, lse = _dense_run(t)
+    for _ in range(3):
+        again, _ = _dense_run(t)
+        assert torch.equal(again, out)
+    want, wlse = torch.zeros(5, h, d).double(), torch.full((5, h), -math.inf).double()
+    mag, size = torch.zeros(5, h, d).double(), torch.zeros(5, h).double()
+    for bi, n in enumerate(lens):
+        if n == 0:
+            continue
+        pages = t["block_table"][bi, :-(-n // 64)].long()
+        for hi in range(h):
+            k, v = (t[x][pages, hi // (h // g)].reshape(-1, d)[:n].double() for x in ("k_pages", "v_pages"))
+            qr = t["q"][bi, hi].double()
+            s = k @ qr * d ** -0.5
+            p = torch.softmax(s, 0)
+            wlse[bi, hi], want[bi, hi], mag[bi, hi] = torch.logsumexp(s, 0), p @ v, p @ v.abs()
+            size[bi, hi] = (k.abs() @ qr.abs()).max() * d ** -0.5
+    want, wlse, mag, size = (x.numpy() for x in (want, wlse, mag, size))
+    # sums run over at most a few thousand terms at a time (16-key slices, warps, SMs): n = 4096
+    r = 2 * d * 2.0 ** -23 * size + 2.0 ** -16 + 4096 * 2.0 ** -23
+    _close(out, want, r[..., None] * mag + _u(out.dtype) * (np.abs(want) + r[..., None] * mag), "out")
+    _close(lse, wlse, r + 2.0 ** -22 * np.abs(np.where(np.isfinite(wlse), wlse, 0)), "lse")
+
+
 def test_dense_every_length_of_a_ragged_batch():
     lens = list(range(0, 260)) + [1500, 3]
     t, w = _dense_case(lens, 2, 1, 64, "bf16", seed=11)
