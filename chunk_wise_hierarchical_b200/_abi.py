@@ -42,6 +42,19 @@ class Shape(ctypes.Structure):
     ]
 
 
+_SHAPES = {}
+
+
+def _shape_of(*key):
+    """make_shape's struct for these arguments, made once (the C side only reads it)."""
+    s = _SHAPES.get(key)
+    if s is None:
+        if len(_SHAPES) > 4096:
+            _SHAPES.clear()
+        s = _SHAPES[key] = make_shape(*key)
+    return s
+
+
 class Rows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("token_stride", ctypes.c_int64)]
@@ -139,6 +152,8 @@ def _stream(stream):
 def _expect(t, shape, dtypes, name):
     """Raises unless tensor t has exactly this shape and one of these dtypes: the kernels
     read every tensor at the extent the shape implies."""
+    if t is not None and t.shape == shape and (dtypes is None or t.dtype in dtypes):
+        return
     if t is None:
         raise ValueError(f"{name} is required")
     if tuple(t.shape) != tuple(shape):
@@ -148,8 +163,9 @@ def _expect(t, shape, dtypes, name):
 
 
 def _same_device(ref, *ts):
+    dev = ref.device
     for t in ts:
-        if t is not None and t.device != ref.device:
+        if t is not None and t.device != dev:
             raise ValueError("every tensor must be on q's device")
 
 
@@ -460,6 +476,10 @@ def backward(q, k, v, landmark, out, lse, topk_idx, topk_score, dout, scale=None
 # ---- the paged cache around the method: rotation, appended tokens, dense layers ----
 
 _FLOATS = (torch.bfloat16, torch.float32)
+# The device and stream that a launch finds, without the Python objects around them: these
+# calls come once per decoded token.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 class _on:
@@ -512,60 +532,58 @@ def _dense_shape(batch, heads_q, heads_kv, head_dim, max_chunks, dtype, scale=No
                       HILS_BF16 if dtype in (torch.bfloat16, "bf16") else HILS_F32, scale=scale or 0.0, window=window)
 
 
-def _rows(t, name, packed=False):
-    """t as hils_rows: [b, heads, n, d], or packed [tokens, heads, d]; any strides whose rows
-    are 16-byte aligned and contiguous."""
-    if t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    st = [x if n > 1 else 0 for x, n in zip(t.stride(), t.shape)]  # a single entry needs no stride
-    r = Rows(t.data_ptr(), 0, st[1], st[0]) if packed else Rows(t.data_ptr(), st[0], st[1], st[2])
-    e = t.element_size()
-    if ((r.data or 0) | r.batch_stride * e | r.head_stride * e | r.token_stride * e) & 15:
-        raise ValueError(f"{name}: rows must be 16-byte aligned (data pointer and strides)")
-    return r
-
-
-def _span(t):
-    """First and last byte address of t's elements (t is not empty)."""
-    n = sum((x - 1) * s for x, s in zip(t.shape, t.stride()))
-    p = t.data_ptr()
-    return p, p + (n + 1) * t.element_size() - 1
-
-
-def _check_written(out, name, *others, itself=None):
-    """A written tensor is contiguous memory apart from the others, or `itself` in place."""
-    if itself is not None and out.data_ptr() == itself.data_ptr() and out.stride() == itself.stride() \
-            and out.dtype == itself.dtype:
-        if any(s == 0 and n > 1 for n, s in zip(out.shape, out.stride())):
-            raise ValueError(f"{name}: an expanded tensor cannot be written in place")
-    elif not out.is_contiguous():
-        raise ValueError(f"{name} must be contiguous, or its input itself")
+def _launch(fn, where, t, stream, *args):
+    """fn(*args, stream) on tensor t's device and, unless `stream` is given, its current stream."""
+    dev = t.get_device()
+    if stream is None and dev >= 0 and _current_device() == dev:
+        st = fn(*args, _raw_stream(dev))
     else:
-        others = (*others, itself)
-    if out.numel() == 0:
-        return
-    a0, a1 = _span(out)
-    for t in others:
-        if t is not None and t.numel():
-            b0, b1 = _span(t)
-            if a0 <= b1 and b0 <= a1:
-                raise ValueError(f"{name} overlaps another tensor of the call")
+        with _on(t, stream) as raw:
+            st = fn(*args, raw)
+    if st != 0:
+        raise HilsError(st, where)
 
 
-def _rope(inv_freq, interleaved, d):
-    if inv_freq is None:
+def _at(t):
+    """The address of a dense tensor (0: none).  Its device has been compared with that of the
+    tensor that the call is launched on."""
+    if t is None:
         return None
+    if not t.is_contiguous():
+        raise ValueError("tensor must be contiguous")
+    return t.data_ptr()
+
+
+def _empty(shape, dtype, t, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=t.device)
+    with _on(t, stream):
+        return torch.empty(shape, dtype=dtype, device=t.device)
+
+
+# hils_rows and hils_rope structs of a call, packed into one array of 8-byte words (a hils_rows
+# is 4 words; a hils_rope 2: the pointer, then rotary_dim | interleaved << 32).
+_Words = {n: ctypes.c_int64 * n for n in (8, 10, 16, 18)}
+
+
+def _rope_words(inv_freq, interleaved, d):
     if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous():
         raise TypeError("inv_freq must be a contiguous fp32 vector")
     r = 2 * inv_freq.numel()
     if r == 0 or r > d or r % 16:
         raise ValueError(f"inv_freq must have a multiple of 8 entries, at most head_dim / 2; got {r // 2}")
-    return Rope(inv_freq.data_ptr(), r, 1 if interleaved else 0)
+    return inv_freq.data_ptr(), r | (1 << 32 if interleaved else 0)
+
+
+def _last_contiguous(*named):
+    for name, t in named:
+        if t is not None and t.stride(-1) != 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
 
 
 def check_rotate_args(q, inv_freq, k=None, positions=None, q_out=None, k_out=None):
     """The tensors of rotate against one another; returns the stride of positions over the
-    batch (0: shared)."""
+    batch (0: shared).  Alignment and overlaps are checked by hils_rotate."""
     if q.dim() != 4:
         raise ValueError("q must be [b, heads_q, n, d]")
     b, _, n, d = q.shape
@@ -573,20 +591,17 @@ def check_rotate_args(q, inv_freq, k=None, positions=None, q_out=None, k_out=Non
         raise TypeError(f"q must be bf16 or fp32, got {q.dtype}")
     if inv_freq is None:
         raise ValueError("inv_freq is required")
-    out_dtypes = _FLOATS
     if q_out is not None:
         _expect(q_out, q.shape, _FLOATS, "q_out")
-        _check_written(q_out, "q_out", k, positions, inv_freq, itself=q)
-        out_dtypes = (q_out.dtype,)
     if k is not None:
         if k.dim() != 4:
             raise ValueError("k must be [b, heads_kv, n, d]")
         _expect(k, (b, k.shape[1], n, d), (q.dtype,), "k")
         if k_out is not None:
-            _expect(k_out, k.shape, out_dtypes if q_out is not None else (q.dtype,), "k_out")
-            _check_written(k_out, "k_out", q, q_out, positions, inv_freq, itself=k)
+            _expect(k_out, k.shape, (q.dtype if q_out is None else q_out.dtype,), "k_out")
     elif k_out is not None:
         raise ValueError("k_out without k")
+    _last_contiguous(("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out))
     _same_device(q, inv_freq, k, positions, q_out, k_out)
     if positions is None:
         return 0
@@ -607,24 +622,29 @@ def rotate(q, inv_freq, k=None, positions=None, inverse=False, interleaved=False
     is (f, f + rotary_dim / 2), or (2f, 2f + 1) when interleaved; elements from rotary_dim on
     are copied.  positions: None (token i at position i), int32 [n], or int32 [b, n].
     inverse: the opposite rotation, which takes the gradients of the rotated q and k (backward's
-    dq and dk) to those of the unrotated ones.  q and k may be slices with any strides whose rows
-    are 16-byte aligned; an output may be its input (in place), and may be bf16 or fp32."""
+    dq and dk) to those of the unrotated ones.  The tensors may have any strides whose rows are
+    contiguous and 16-byte aligned; an output may be its input (in place), and may be bf16 or
+    fp32 whatever the input is."""
     pstride = check_rotate_args(q, inv_freq, k, positions, q_out, k_out)
     b, h, n, d = q.shape
-    rope = _rope(inv_freq, interleaved, d)
-    ref = ctypes.byref
-    with _on(q, stream) as st:
-        if q_out is None:
-            q_out = torch.empty((b, h, n, d), dtype=q.dtype, device=q.device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=q_out.dtype, device=q.device)
-        if q_out.numel() and (k is None or k.numel()):
-            sh = make_shape(b, h, h if k is None else k.shape[1], d, n, 0, _dt(q))
-            _check(lib().hils_rotate(ref(sh), ref(_rows(q, "q")), None if k is None else ref(_rows(k, "k")), ref(rope),
-                                     None if positions is None else positions.data_ptr(), pstride,
-                                     1 if inverse else 0, ref(_rows(q_out, "q_out")),
-                                     None if k is None else ref(_rows(k_out, "k_out")), _dt(q_out), st),
-                   "hils_rotate")
+    if q_out is None:
+        q_out = _empty(q.shape, q.dtype, q, stream)
+    if k is not None and k_out is None:
+        k_out = _empty(k.shape, q_out.dtype, q, stream)
+    words = _rope_words(inv_freq, interleaved, d)
+    qs, os = q.stride(), q_out.stride()
+    words += (q.data_ptr(), qs[0], qs[1], qs[2], q_out.data_ptr(), os[0], os[1], os[2])
+    g = h
+    if k is not None:
+        g = k.shape[1]
+        qs, os = k.stride(), k_out.stride()
+        words += (k.data_ptr(), qs[0], qs[1], qs[2], k_out.data_ptr(), os[0], os[1], os[2])
+    if b * n * h * g:
+        w = _Words[len(words)](*words)
+        at = ctypes.addressof(w)
+        _launch(lib().hils_rotate, "hils_rotate", q, stream, _shape_of(b, h, g, d, n, 0, _dt(q)), at + 16,
+                None if k is None else at + 80, at, None if positions is None else positions.data_ptr(), pstride,
+                1 if inverse else 0, at + 48, None if k is None else at + 112, _dt(q_out))
     return q_out if k is None else (q_out, k_out)
 
 
@@ -636,7 +656,8 @@ def append_slots(batch, tokens):
 
 def check_append_args(shape, k, v, k_pages, v_pages, block_table, max_chunks, seq_lens, q=None, q_out=None,
                       cu_new=None, new_lens=None, full_pages=None):
-    """The tensors of an append against the shape (see Append.__call__)."""
+    """The tensors of an append against the shape (see Append.__call__).  Alignment and
+    overlaps are checked by hils_append_paged."""
     b, h, g, d = shape.batch, shape.heads_q, shape.heads_kv, shape.head_dim
     dts = (torch.bfloat16 if shape.dtype == HILS_BF16 else torch.float32,)
     if k.dim() == 3:
@@ -669,11 +690,11 @@ def check_append_args(shape, k, v, k_pages, v_pages, block_table, max_chunks, se
         _expect(q, qrows, dts, "q")
         if q_out is not None:
             _expect(q_out, qrows, dts, "q_out")
-            _check_written(q_out, "q_out", k, v, k_pages, v_pages, itself=q)
     elif q_out is not None:
         raise ValueError("q_out without q")
     if full_pages is not None:
         _expect(full_pages, (append_slots(b, tokens),), (torch.int32,), "full_pages")
+    _last_contiguous(("k", k), ("v", v), ("q", q), ("q_out", q_out))
     _same_device(k, v, q, q_out, k_pages, v_pages, block_table, seq_lens, cu_new, new_lens, full_pages)
 
 
@@ -687,7 +708,7 @@ class Append:
         self.max_chunks = max_chunks
         self.shape = _dense_shape(batch, heads_q, heads_kv, head_dim, max_chunks, dtype)
         self.inv_freq = inv_freq
-        self.rope = _rope(inv_freq, interleaved, head_dim)
+        self.rope = None if inv_freq is None else _Words[10](*_rope_words(inv_freq, interleaved, head_dim))
         self.ws = _own_workspace(self.shape, OP_APPEND, device, ws)
         _same_device(self.ws, inv_freq)
 
@@ -701,27 +722,32 @@ class Append:
         cu_new [b+1] int32 gives each sequence's rows, or None: one token per sequence.
         seq_lens [b] int32 are the lengths after the call.  full_pages: int32
         [append_slots(b, tokens)], receives the pages filled by the call, else -1: it can go to
-        summarize_paged as it is."""
+        summarize_paged as it is.  q_out may be q itself."""
         s = self.shape
         check_append_args(s, k, v, k_pages, v_pages, block_table, self.max_chunks, seq_lens, q, q_out, cu_new,
                           new_lens, full_pages)
         _same_device(k, self.ws)
-        ref = ctypes.byref
-        packed = cu_new is not None
-        single = k.dim() == 3 and not packed  # one token per sequence: [b, heads, 1, d]
+        if q is not None and q_out is None:
+            q_out = _empty(q.shape, q.dtype, k, stream)
+        packed = k.dim() == 3
 
-        def rows_of(t, name):
-            return None if t is None else ref(_rows(t.unsqueeze(2) if single else t, name, packed))
+        def words(t):
+            st = t.stride()
+            if not packed:
+                return t.data_ptr(), st[0], st[1], st[2]
+            # one row per token; without cu_new the tokens are the batch, one each
+            return (t.data_ptr(), 0, st[1], st[0]) if cu_new is not None else (t.data_ptr(), st[0], st[1], 0)
 
-        with _on(k, stream) as st:
-            if q is not None and q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            _check(lib().hils_append_paged(
-                ref(s), rows_of(k, "k"), rows_of(v, "v"), rows_of(q, "q"), rows_of(q_out, "q_out"),
-                1 if single else k.shape[0] if packed else k.shape[2], _ptr(cu_new), _ptr(new_lens), _ptr(seq_lens),
-                _ptr(block_table), self.max_chunks, k_pages.shape[0], None if self.rope is None else ref(self.rope),
-                _ptr(k_pages), _ptr(v_pages), _ptr(full_pages), _ptr(self.ws), self.ws.numel(), st),
-                "hils_append_paged")
+        w = words(k) + words(v)
+        if q is not None:
+            w += words(q) + words(q_out)
+        w = _Words[len(w)](*w)
+        at = ctypes.addressof(w)
+        n_new = k.shape[2] if not packed else 1 if cu_new is None else k.shape[0]
+        _launch(lib().hils_append_paged, "hils_append_paged", k, stream, s, at, at + 32,
+                None if q is None else at + 64, None if q is None else at + 96, n_new, _at(cu_new), _at(new_lens),
+                _at(seq_lens), _at(block_table), self.max_chunks, k_pages.shape[0], self.rope, _at(k_pages),
+                _at(v_pages), _at(full_pages), _at(self.ws), self.ws.numel())
         return q_out
 
     def device_status(self, stream=None):
@@ -775,13 +801,11 @@ class DenseDecode:
         """out [b,h,d] (q's dtype); lse, if given (fp32 [b,h]), receives log sum exp(logit)."""
         check_dense_args(self.shape, q, k_pages, v_pages, block_table, self.max_chunks, seq_lens, out, lse)
         _same_device(q, self.ws)
-        with _on(q, stream) as st:
-            if out is None:
-                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            _check(lib().hils_decode_dense(ctypes.byref(self.shape), _ptr(q), _ptr(k_pages), _ptr(v_pages),
-                                           _ptr(block_table), self.max_chunks, _ptr(seq_lens), k_pages.shape[0],
-                                           _ptr(out), _ptr(lse), _ptr(self.ws), self.ws.numel(), st),
-                   "hils_decode_dense")
+        if out is None:
+            out = _empty(q.shape, q.dtype, q, stream)
+        _launch(lib().hils_decode_dense, "hils_decode_dense", q, stream, self.shape, _at(q), _at(k_pages),
+                _at(v_pages), _at(block_table), self.max_chunks, _at(seq_lens), k_pages.shape[0], _at(out), _at(lse),
+                _at(self.ws), self.ws.numel())
         return out
 
     def device_status(self, stream=None):

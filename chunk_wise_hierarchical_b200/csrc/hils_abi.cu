@@ -6,6 +6,7 @@
 #include <cstring>
 #include <atomic>
 #include <mutex>
+#include <utility>
 
 #include "../../include/hils.h"
 #include "common.cuh"
@@ -197,13 +198,46 @@ cudaError_t run_prefill_attention(const hils_shape* s, const void* q, const void
   return hils::run_attend_rows(ar, cs);
 }
 
-// Rows that 16-byte loads and stores can take.
-hils_status check_rows(const hils_rows* r, size_t elem) {
-  if (!r || !r->data) return HILS_ERR_INVALID_ARG;
-  if (!aligned16(r->data) || r->batch_stride * (long long)elem % 16 != 0 || r->head_stride * (long long)elem % 16 != 0 ||
-      r->token_stride * (long long)elem % 16 != 0)
-    return HILS_ERR_INVALID_ARG;
+// Rows of (nb, nh, nt) x d elements that 16-byte loads and stores can take (the stride of a
+// dimension with one entry is not looked at).
+hils_status check_rows(const hils_rows* r, long long nb, long long nh, long long nt, size_t elem) {
+  if (!r || !r->data || !aligned16(r->data)) return HILS_ERR_INVALID_ARG;
+  const long long n[3] = {nb, nh, nt}, st[3] = {r->batch_stride, r->head_stride, r->token_stride};
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1 && (st[i] < 0 || st[i] * (long long)elem % 16 != 0)) return HILS_ERR_INVALID_ARG;
   return HILS_OK;
+}
+// Bytes [lo, hi) that rows of (nb, nh, nt) x d elements lie in.
+struct Span {
+  uintptr_t lo, hi;
+};
+Span span_of(const hils_rows* r, long long nb, long long nh, long long nt, int d, size_t elem) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(r->data);
+  if (nb == 0 || nh == 0 || nt == 0) return {p, p};
+  return {p, p + (size_t)((nb - 1) * r->batch_stride + (nh - 1) * r->head_stride + (nt - 1) * r->token_stride + d) * elem};
+}
+bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+// Whether no two rows of a written tensor share an element: by ascending stride, each
+// dimension steps over all that the dimensions below it cover.
+bool rows_apart(const hils_rows* r, long long nb, long long nh, long long nt, int d) {
+  long long n[3] = {nb, nh, nt}, st[3] = {r->batch_stride, r->head_stride, r->token_stride}, extent = d;
+  for (int i = 0; i < 2; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (st[j] < st[i]) {
+        std::swap(st[i], st[j]);
+        std::swap(n[i], n[j]);
+      }
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] <= 1) continue;
+    if (st[i] < extent) return false;
+    extent += st[i] * (n[i] - 1);
+  }
+  return true;
+}
+// Whether out is in's own memory, element for element.
+bool in_place(const hils_rows* out, const hils_rows* in, long long nb, long long nh, long long nt) {
+  return out->data == in->data && (nb <= 1 || out->batch_stride == in->batch_stride) &&
+         (nh <= 1 || out->head_stride == in->head_stride) && (nt <= 1 || out->token_stride == in->token_stride);
 }
 hils_status check_rope(const hils_rope* r, int head_dim) {
   if (!r || !r->inv_freq || (reinterpret_cast<uintptr_t>(r->inv_freq) & 3u) != 0) return HILS_ERR_INVALID_ARG;
@@ -489,11 +523,30 @@ hils_status hils_rotate(const hils_shape* s, const hils_rows* q, const hils_rows
   if (position_stride < 0) return HILS_ERR_INVALID_ARG;
   if ((st = check_rope(rope, s->head_dim)) != HILS_OK) return st;
   if ((size_t)s->batch * s->seq_len == 0) return HILS_OK;
-  if ((st = check_rows(q, elem_size(s->dtype))) != HILS_OK || (st = check_rows(q_out, elem_size(out_dtype))) != HILS_OK)
-    return st;
-  if (k && ((st = check_rows(k, elem_size(s->dtype))) != HILS_OK ||
-            (st = check_rows(k_out, elem_size(out_dtype))) != HILS_OK))
-    return st;
+  {
+    const long long nb = s->batch, nt = s->seq_len;
+    const size_t ei = elem_size(s->dtype), eo = elem_size(out_dtype);
+    if ((st = check_rows(q, nb, s->heads_q, nt, ei)) != HILS_OK ||
+        (st = check_rows(q_out, nb, s->heads_q, nt, eo)) != HILS_OK)
+      return st;
+    if (k && ((st = check_rows(k, nb, s->heads_kv, nt, ei)) != HILS_OK ||
+              (st = check_rows(k_out, nb, s->heads_kv, nt, eo)) != HILS_OK))
+      return st;
+    // each output apart from every other tensor, its own input in place excepted
+    const Span none{0, 0};
+    const Span qi = span_of(q, nb, s->heads_q, nt, s->head_dim, ei), qo = span_of(q_out, nb, s->heads_q, nt, s->head_dim, eo);
+    const Span ki = k ? span_of(k, nb, s->heads_kv, nt, s->head_dim, ei) : none;
+    const Span ko = k ? span_of(k_out, nb, s->heads_kv, nt, s->head_dim, eo) : none;
+    const bool q_same = ei == eo && in_place(q_out, q, nb, s->heads_q, nt);
+    const bool k_same = k && ei == eo && in_place(k_out, k, nb, s->heads_kv, nt);
+    if (!rows_apart(q_out, nb, s->heads_q, nt, s->head_dim) ||
+        (k && !rows_apart(k_out, nb, s->heads_kv, nt, s->head_dim)))
+      return HILS_ERR_INVALID_ARG;
+    // slices of one fused tensor interleave: in place, q_out may lie between k's rows
+    if ((!q_same && (overlap(qo, qi) || overlap(qo, ki))) || (!k_same && (overlap(ko, ki) || overlap(ko, qi))) ||
+        (!(q_same && k_same) && overlap(qo, ko)))
+      return HILS_ERR_INVALID_ARG;
+  }
   hils::RotateArgs a{};
   a.in[0] = rows_of(q); a.out[0] = rows_of(q_out); a.heads[0] = s->heads_q;
   if (k) { a.in[1] = rows_of(k); a.out[1] = rows_of(k_out); a.heads[1] = s->heads_kv; }
@@ -522,8 +575,28 @@ hils_status hils_append_paged(const hils_shape* s, const hils_rows* k, const hil
   const size_t es = elem_size(s->dtype);
   if (tokens > 0) {
     if (!k_pages || !v_pages || !aligned16(k_pages) || !aligned16(v_pages)) return HILS_ERR_INVALID_ARG;
-    if ((st = check_rows(k, es)) != HILS_OK || (st = check_rows(v, es)) != HILS_OK) return st;
-    if (q && ((st = check_rows(q, es)) != HILS_OK || (st = check_rows(q_out, es)) != HILS_OK)) return st;
+    const long long nb = cu_new ? 1 : s->batch;
+    if ((st = check_rows(k, nb, s->heads_kv, n_new, es)) != HILS_OK ||
+        (st = check_rows(v, nb, s->heads_kv, n_new, es)) != HILS_OK)
+      return st;
+    if (q && ((st = check_rows(q, nb, s->heads_q, n_new, es)) != HILS_OK ||
+              (st = check_rows(q_out, nb, s->heads_q, n_new, es)) != HILS_OK))
+      return st;
+    const size_t pool = (size_t)n_pages * s->heads_kv * s->chunk * s->head_dim * es;
+    const Span kp{reinterpret_cast<uintptr_t>(k_pages), reinterpret_cast<uintptr_t>(k_pages) + pool};
+    const Span vp{reinterpret_cast<uintptr_t>(v_pages), reinterpret_cast<uintptr_t>(v_pages) + pool};
+    const Span ki = span_of(k, nb, s->heads_kv, n_new, s->head_dim, es);
+    const Span vi = span_of(v, nb, s->heads_kv, n_new, s->head_dim, es);
+    if (overlap(kp, vp) || overlap(kp, ki) || overlap(kp, vi) || overlap(vp, ki) || overlap(vp, vi))
+      return HILS_ERR_INVALID_ARG;
+    if (q) {
+      const Span qi = span_of(q, nb, s->heads_q, n_new, s->head_dim, es);
+      const Span qo = span_of(q_out, nb, s->heads_q, n_new, s->head_dim, es);
+      if (!rows_apart(q_out, nb, s->heads_q, n_new, s->head_dim)) return HILS_ERR_INVALID_ARG;
+      if (overlap(qo, kp) || overlap(qo, vp) || overlap(qi, kp) || overlap(qi, vp) ||
+          (!in_place(q_out, q, nb, s->heads_q, n_new) && (overlap(qo, qi) || overlap(qo, ki) || overlap(qo, vi))))
+        return HILS_ERR_INVALID_ARG;
+    }
   } else if (!full_pages) {
     return HILS_OK;
   }

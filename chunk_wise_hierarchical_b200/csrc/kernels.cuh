@@ -222,9 +222,9 @@ struct RotateArgs {
   long long position_stride;
   int b, n, d, rot;
   bool interleaved, inverse, in_bf16, out_bf16;
-  int tile, head_block;       // tokens and heads of a CTA (set by the launcher)
+  int head_block;             // heads of a CTA (set by the launcher)
 };
-cudaError_t run_rotate(RotateArgs a, cudaStream_t st);
+cudaError_t run_rotate(const RotateArgs& a, cudaStream_t st);
 
 struct AppendArgs {
   Rows q, q_out, k, v;
@@ -243,9 +243,9 @@ struct AppendArgs {
   int32_t* full_pages;        // [n_slots] or nullptr
   int n_slots;
   unsigned* err;
-  int tile, head_block;       // set by the launcher
+  int head_block;             // set by the launcher
 };
-cudaError_t run_append(AppendArgs a, cudaStream_t st);
+cudaError_t run_append(const AppendArgs& a, cudaStream_t st);
 
 struct DenseArgs {
   const void* q;

@@ -9,11 +9,12 @@
 // radians at the positions of a long cache -- and only its remainder, at most half a turn,
 // is rounded to fp32 for sincospif.
 //
-// Both kernels are bound by HBM: every element is read once and written once.  A CTA takes a
-// tile of tokens and a block of heads, computes the tile's cosines and sines once into
-// shared memory (all its heads use them), and then moves 32 bytes a thread and step: a unit
-// is 2 E elements (E = 16 bytes' worth), either E adjacent pairs, or E elements of the
-// first half of the rotated part with their E partners, or 2 E elements that are copied.
+// Both kernels are bound by HBM: every element is read once and written once.  A thread owns
+// one unit of one token -- 2 E elements of its row (E = 16 bytes' worth): E pairs, or 2 E
+// elements that are copied -- in every head of its block.  It computes the cosines and sines
+// of its pairs once, keeps them in registers, and walks the heads, so that a head costs two
+// loads, the products and two stores.  The tokens of the whole batch are numbered in a row, and
+// a CTA takes kRotThreads / (units per row) of them: short sequences fill it as long ones do.
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -21,10 +22,10 @@ namespace hils {
 
 namespace {
 
-constexpr int kRotThreads = 256;
-constexpr int kRotTile = 32;      // tokens per CTA, at most
-constexpr int kRotUnits = 4;      // units a thread loads before it stores the first
-constexpr int kRotCtas = 4 * 148; // CTAs wanted before tiles are made smaller
+constexpr int kRotThreads = 128;
+constexpr int kRotHeads = 4;       // heads whose loads a thread issues before it stores the first
+constexpr int kRotCtas = 2 * 148;  // CTAs wanted before a block of heads is made smaller
+constexpr int kRotSeqs = 1024;     // sequences whose row offsets fit shared memory
 
 __device__ __forceinline__ float2 turn_of(int pos, float w) {
   double t = (double)pos * (double)w * 0.15915494309189533577;  // 1 / (2 pi)
@@ -82,50 +83,61 @@ __device__ __forceinline__ void unit_offsets(int u, int rot, bool interleaved, i
   o1 = halves ? o0 + rot / 2 : o0 + E;
 }
 
-// Turns one unit and stores it.  cs: the token's (cos, sin) by frequency.
-template <typename Tin, typename Tout>
-__device__ __forceinline__ void turn_unit(const uint4& r0, const uint4& r1, int u, int rot, bool interleaved,
-                                          const float2* cs, Tout* row) {
-  constexpr int E = Unit<Tin>::E;
-  int o0, o1;
-  unit_offsets<E>(u, rot, interleaved, o0, o1);
+// The cosines and sines of one unit's pairs, and how its pieces pair up.
+enum { kCopied = 0, kHalves = 1, kAdjacent = 2 };
+template <int E>
+struct Turns {
+  float2 w[E];
+  int how;
+  __device__ __forceinline__ void set(int pos, const float* inv_freq, int u, int rot, bool interleaved, bool inverse) {
+    how = u >= rot / (2 * E) ? kCopied : interleaved ? kAdjacent : kHalves;
+    if (how == kCopied) return;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {  // pair u E + i, whichever way the pairs are laid out
+      w[i] = turn_of(pos, __ldg(inv_freq + u * E + i));
+      if (inverse) w[i].y = -w[i].y;
+    }
+  }
+};
+
+// Turns one unit's two pieces and stores them.
+template <typename Tin, typename Tout, int E = Unit<Tin>::E>
+__device__ __forceinline__ void turn_unit(const uint4& r0, const uint4& r1, const Turns<E>& t, Tout* d0, Tout* d1) {
+  if (sizeof(Tin) == sizeof(Tout) && t.how == kCopied) {  // bit for bit
+    *reinterpret_cast<uint4*>(d0) = r0;
+    *reinterpret_cast<uint4*>(d1) = r1;
+    return;
+  }
   float a[E], b[E];
   unpack<Tin>(r0, a);
   unpack<Tin>(r1, b);
-  if (u < rot / (2 * E)) {
-    if (interleaved) {
+  if (t.how == kAdjacent) {
 #pragma unroll
-      for (int i = 0; i < E; i += 2) {
-        const float2 w0 = cs[u * E + i / 2], w1 = cs[u * E + E / 2 + i / 2];
-        const float x0 = a[i], y0 = a[i + 1], x1 = b[i], y1 = b[i + 1];
-        a[i] = x0 * w0.x - y0 * w0.y;
-        a[i + 1] = y0 * w0.x + x0 * w0.y;
-        b[i] = x1 * w1.x - y1 * w1.y;
-        b[i + 1] = y1 * w1.x + x1 * w1.y;
-      }
-    } else {
+    for (int i = 0; i < E; i += 2) {
+      const float2 w0 = t.w[i / 2], w1 = t.w[E / 2 + i / 2];
+      const float x0 = a[i], y0 = a[i + 1], x1 = b[i], y1 = b[i + 1];
+      a[i] = x0 * w0.x - y0 * w0.y;
+      a[i + 1] = y0 * w0.x + x0 * w0.y;
+      b[i] = x1 * w1.x - y1 * w1.y;
+      b[i + 1] = y1 * w1.x + x1 * w1.y;
+    }
+  } else if (t.how == kHalves) {
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const float2 w = cs[u * E + i];
-        const float x = a[i], y = b[i];
-        a[i] = x * w.x - y * w.y;
-        b[i] = y * w.x + x * w.y;
-      }
+    for (int i = 0; i < E; ++i) {
+      const float x = a[i], y = b[i];
+      a[i] = x * t.w[i].x - y * t.w[i].y;
+      b[i] = y * t.w[i].x + x * t.w[i].y;
     }
   }
-  store<Tout>(row + o0, a);
-  store<Tout>(row + o1, b);
+  store<Tout>(d0, a);
+  store<Tout>(d1, b);
 }
 
-// Tokens of a tile and heads of a block so that about kRotCtas CTAs have work: long inputs
-// get full tiles and every head (the cosines are computed once); few tokens are spread over
-// the SMs, tokens first, then heads.
-void pick_tile(long long tokens, int heads, int* tile, int* head_block) {
-  int t = kRotTile, hb = heads;
-  while (t > 1 && (tokens + t - 1) / t < kRotCtas) t >>= 1;
-  while (hb > 1 && (tokens + t - 1) / t * ((heads + hb - 1) / hb) < kRotCtas && (long long)t * hb > 8) hb = (hb + 1) / 2;
-  *tile = t;
-  *head_block = hb;
+// Heads per CTA: all of them (the angles are computed once) unless that leaves SMs idle.
+int pick_heads(long long token_blocks, int heads) {
+  int hb = heads;
+  while (hb > 1 && token_blocks * ((heads + hb - 1) / hb) < kRotCtas) hb = (hb + 1) / 2;
+  return hb;
 }
 
 }  // namespace
@@ -135,70 +147,64 @@ template <typename Tin, typename Tout, int D>
 __global__ void __launch_bounds__(kRotThreads) rotate_kernel(RotateArgs a) {
   constexpr int E = Unit<Tin>::E;
   constexpr int U = D / (2 * E);  // units per row
-  __shared__ float2 s_cs[kRotTile][D / 2];
-  const int t = threadIdx.x;
   const int heads = a.heads[0] + a.heads[1];
   const int n_hb = (heads + a.head_block - 1) / a.head_block;
-  const int n_tile = (a.n + a.tile - 1) / a.tile;
-  const int h0 = (int)(blockIdx.x % n_hb) * a.head_block;
-  const int ti = (int)(blockIdx.x / n_hb) % n_tile;
-  const int bi = (int)(blockIdx.x / n_hb) / n_tile;
-  const int t0 = ti * a.tile, nt = min(a.tile, a.n - t0), nh = min(a.head_block, heads - h0);
-  const int nf = a.rot / 2;
-  for (int x = t; x < nt * nf; x += kRotThreads) {
-    const int tok = x / nf, f = x % nf;
-    const int pos = a.positions ? a.positions[bi * a.position_stride + t0 + tok] : t0 + tok;
-    float2 w = turn_of(pos, a.inv_freq[f]);
-    if (a.inverse) w.y = -w.y;
-    s_cs[tok][f] = w;
-  }
-  __syncthreads();
-  const int total = nh * a.tile * U;
-  for (int x0 = t; x0 < total; x0 += kRotThreads * kRotUnits) {
-    uint4 r0[kRotUnits], r1[kRotUnits];
+  const int h0 = (int)(blockIdx.x % n_hb) * a.head_block, h1 = min(heads, h0 + a.head_block);
+  const int u = threadIdx.x % U;
+  const long long row = (long long)(blockIdx.x / n_hb) * (kRotThreads / U) + threadIdx.x / U;
+  if (row >= (long long)a.b * a.n) return;
+  const int bi = (int)(row / a.n), i = (int)(row % a.n);
+  int o0, o1;
+  unit_offsets<E>(u, a.rot, a.interleaved, o0, o1);
+  const Tin* src[2];
+  Tout* dst[2];
 #pragma unroll
-    for (int k = 0; k < kRotUnits; ++k) {
-      const int x = x0 + k * kRotThreads;
-      const int u = x % U, tok = x / U % a.tile, hh = h0 + x / U / a.tile;
-      if (x < total && tok < nt) {
-        const int which = hh >= a.heads[0];
-        const Rows& R = a.in[which];
-        const Tin* row = static_cast<const Tin*>(R.data) + bi * R.batch_stride +
-                         (hh - which * a.heads[0]) * R.head_stride + (t0 + tok) * R.token_stride;
-        int o0, o1;
-        unit_offsets<E>(u, a.rot, a.interleaved, o0, o1);
-        r0[k] = *reinterpret_cast<const uint4*>(row + o0);
-        r1[k] = *reinterpret_cast<const uint4*>(row + o1);
+  for (int w = 0; w < 2; ++w) {
+    src[w] = static_cast<const Tin*>(a.in[w].data) + bi * a.in[w].batch_stride + i * a.in[w].token_stride;
+    dst[w] = static_cast<Tout*>(a.out[w].data) + bi * a.out[w].batch_stride + i * a.out[w].token_stride;
+  }
+  const int pos = a.positions ? a.positions[bi * a.position_stride + i] : i;
+  Turns<E> t;
+  t.set(pos, a.inv_freq, u, a.rot, a.interleaved, a.inverse);
+  for (int h = h0; h < h1; h += kRotHeads) {
+    uint4 r0[kRotHeads], r1[kRotHeads];
+#pragma unroll
+    for (int k = 0; k < kRotHeads; ++k) {
+      const int hh = h + k, w = hh >= a.heads[0];
+      if (hh < h1) {
+        const Tin* p = src[w] + (hh - (w ? a.heads[0] : 0)) * a.in[w].head_stride;
+        r0[k] = *reinterpret_cast<const uint4*>(p + o0);
+        r1[k] = *reinterpret_cast<const uint4*>(p + o1);
       }
     }
 #pragma unroll
-    for (int k = 0; k < kRotUnits; ++k) {
-      const int x = x0 + k * kRotThreads;
-      const int u = x % U, tok = x / U % a.tile, hh = h0 + x / U / a.tile;
-      if (x < total && tok < nt) {
-        const int which = hh >= a.heads[0];
-        const Rows& R = a.out[which];
-        Tout* row = static_cast<Tout*>(R.data) + bi * R.batch_stride + (hh - which * a.heads[0]) * R.head_stride +
-                    (t0 + tok) * R.token_stride;
-        turn_unit<Tin, Tout>(r0[k], r1[k], u, a.rot, a.interleaved, s_cs[tok], row);
+    for (int k = 0; k < kRotHeads; ++k) {
+      const int hh = h + k, w = hh >= a.heads[0];
+      if (hh < h1) {
+        Tout* p = dst[w] + (hh - (w ? a.heads[0] : 0)) * a.out[w].head_stride;
+        turn_unit<Tin, Tout>(r0[k], r1[k], t, p + o0, p + o1);
       }
     }
   }
 }
 
-template <typename Tin, typename Tout>
-static cudaError_t launch_rotate(const RotateArgs& a, cudaStream_t st) {
+template <typename Tin, typename Tout, int D>
+static cudaError_t launch_rotate_d(RotateArgs a, cudaStream_t st) {
+  constexpr int kRows = kRotThreads / (D / (2 * Unit<Tin>::E));
   const int heads = a.heads[0] + a.heads[1];
-  const long long blocks =
-      (long long)a.b * ((a.n + a.tile - 1) / a.tile) * ((heads + a.head_block - 1) / a.head_block);
+  const long long token_blocks = ((long long)a.b * a.n + kRows - 1) / kRows;
+  a.head_block = pick_heads(token_blocks, heads);
+  const long long blocks = token_blocks * ((heads + a.head_block - 1) / a.head_block);
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  if (a.d == 64) rotate_kernel<Tin, Tout, 64><<<(unsigned)blocks, kRotThreads, 0, st>>>(a);
-  else rotate_kernel<Tin, Tout, 128><<<(unsigned)blocks, kRotThreads, 0, st>>>(a);
+  rotate_kernel<Tin, Tout, D><<<(unsigned)blocks, kRotThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
+template <typename Tin, typename Tout>
+static cudaError_t launch_rotate(const RotateArgs& a, cudaStream_t st) {
+  return a.d == 64 ? launch_rotate_d<Tin, Tout, 64>(a, st) : launch_rotate_d<Tin, Tout, 128>(a, st);
+}
 
-cudaError_t run_rotate(RotateArgs a, cudaStream_t st) {
-  pick_tile((long long)a.b * a.n, a.heads[0] + a.heads[1], &a.tile, &a.head_block);
+cudaError_t run_rotate(const RotateArgs& a, cudaStream_t st) {
   if (a.in_bf16)
     return a.out_bf16 ? launch_rotate<__nv_bfloat16, __nv_bfloat16>(a, st) : launch_rotate<__nv_bfloat16, float>(a, st);
   return a.out_bf16 ? launch_rotate<float, __nv_bfloat16>(a, st) : launch_rotate<float, float>(a, st);
@@ -207,18 +213,9 @@ cudaError_t run_rotate(RotateArgs a, cudaStream_t st) {
 // ---- hils_append_paged ------------------------------------------------------
 namespace {
 
-// What a CTA knows of a token of its tile.
-struct Token {
-  int live;        // 0: padding, or a token that cannot be placed
-  int bi, i;       // sequence, and token within it
-  int pos;         // position in the cache
-  int page;        // -1: not written to the pages
-};
-
-// The sequence b with cu[b] <= t < cu[b + 1] (the last one with cu[b] <= t; in [0, n) for
-// any values).
+// The last b < n with cu[b] <= t (0 where there is none): the sequence of row t.
 __device__ __forceinline__ int find_seq(const int32_t* cu, int n, int t) {
-  int lo = 0, hi = n;  // cu[lo] <= t < cu[hi], in the sense of a sorted cu
+  int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (cu[mid] <= t) lo = mid;
@@ -229,33 +226,39 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int n, int t) {
 
 }  // namespace
 
+// The CTAs from n_work on write the list of filled pages.
 template <typename T, int D>
-__global__ void __launch_bounds__(kRotThreads) append_kernel(AppendArgs a, int n_work, int n_tile) {
+__global__ void __launch_bounds__(kRotThreads) append_kernel(AppendArgs a, int n_work) {
   constexpr int E = Unit<T>::E;
   constexpr int U = D / (2 * E);
-  __shared__ float2 s_cs[kRotTile][D / 2];
-  __shared__ Token s_tok[kRotTile];
+  __shared__ int32_t s_cu[kRotSeqs + 1];
   const int t = threadIdx.x;
   const bool packed = a.cu_new != nullptr;
+  const int32_t* cu = a.cu_new;
+  if (packed && a.b <= kRotSeqs) {  // the search below reads the offsets one after another
+    for (int x = t; x <= a.b; x += kRotThreads) s_cu[x] = a.cu_new[x];
+    __syncthreads();
+    cu = s_cu;
+  }
 
   if ((int)blockIdx.x >= n_work) {
-    // the list of filled pages: entry s belongs to the sequence b with P_b <= s < P_{b+1},
-    // P_b = b + start_b / B; that is room for every page the sequence's tokens can fill
+    // entry s belongs to the sequence b with P_b <= s < P_{b+1}, P_b = b + start_b / B: that
+    // is room for every page the sequence's tokens can fill
     const int s = ((int)blockIdx.x - n_work) * kRotThreads + t;
     if (s >= a.n_slots) return;
-    auto start = [&](int b) { return packed ? (long long)a.cu_new[b] : (long long)b * a.n_new; };
+    auto start = [&](int b) { return packed ? (long long)cu[b] : (long long)b * a.n_new; };
     int lo = 0, hi = a.b;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (mid + start(mid) / kChunk <= s) lo = mid;
       else hi = mid;
     }
-    int n = packed ? a.cu_new[lo + 1] - a.cu_new[lo] : a.new_lens ? min(a.new_lens[lo], a.n_new) : a.n_new;
-    const long long L = a.seq_lens[lo];
-    const long long pos0 = L - n;
-    const long long c = (pos0 < 0 ? 0 : pos0) / kChunk + (s - lo - start(lo) / kChunk);
+    const int n = packed ? cu[lo + 1] - cu[lo] : a.new_lens ? min(a.new_lens[lo], a.n_new) : a.n_new;
+    const long long L = a.seq_lens[lo], pos0 = L - n;
+    const long long j = s - lo - start(lo) / kChunk;
+    const long long c = (pos0 < 0 ? 0 : pos0) / kChunk + j;
     int page = -1;
-    if (n > 0 && s >= lo + start(lo) / kChunk && c * kChunk + kChunk - 1 < L && c < a.max_chunks) {
+    if (n > 0 && j >= 0 && c * kChunk + kChunk - 1 < L && c < a.max_chunks) {
       page = a.block_table[(size_t)lo * a.max_chunks + c];
       if (page < 0 || page >= a.n_pages) page = -1;
     }
@@ -263,111 +266,90 @@ __global__ void __launch_bounds__(kRotThreads) append_kernel(AppendArgs a, int n
     return;
   }
 
-  const int heads = a.h + 2 * a.g;
+  const int heads = a.h + 2 * a.g;  // the query heads, the key heads, the value heads
   const int n_hb = (heads + a.head_block - 1) / a.head_block;
-  const int h0 = (int)(blockIdx.x % n_hb) * a.head_block;
-  const int ti = (int)(blockIdx.x / n_hb) % n_tile;
-  const int row0 = ti * a.tile;  // first token of the tile: a row, or a token of sequence bz
-  const int bz = (int)(blockIdx.x / n_hb) / n_tile;
-  const int nt = min(a.tile, a.n_new - row0), nh = min(a.head_block, heads - h0);
-  const int nf = a.rot / 2;
-  if (t < nt) {
-    Token k;
-    int n;
-    if (packed) {
-      k.bi = find_seq(a.cu_new, a.b, row0 + t);
-      n = a.cu_new[k.bi + 1] - a.cu_new[k.bi];
-      k.i = row0 + t - a.cu_new[k.bi];
-    } else {
-      k.bi = bz;
-      n = a.new_lens ? min(a.new_lens[bz], a.n_new) : a.n_new;
-      k.i = row0 + t;
-    }
-    const long long pos = (long long)a.seq_lens[k.bi] - n + k.i;
-    k.live = k.i >= 0 && k.i < n;
-    k.pos = (int)pos;
-    k.page = -1;
-    if (k.live) {
-      if (pos >= 0 && pos < (long long)a.max_chunks * kChunk)
-        k.page = a.block_table[(size_t)k.bi * a.max_chunks + k.pos / kChunk];
-      if (k.page < 0 || k.page >= a.n_pages) {
-        k.page = -1;
-        set_error(a.err, kErrBadPage);
-      }
-      if (pos < 0) k.live = 0;
-    }
-    s_tok[t] = k;
+  const int h0 = (int)(blockIdx.x % n_hb) * a.head_block, h1 = min(heads, h0 + a.head_block);
+  const int u = t % U;
+  const long long row = (long long)(blockIdx.x / n_hb) * (kRotThreads / U) + t / U;
+  if (row >= (packed ? (long long)a.n_new : (long long)a.b * a.n_new)) return;
+  const int bi = packed ? find_seq(cu, a.b, (int)row) : (int)(row / a.n_new);
+  const int i = packed ? (int)row - cu[bi] : (int)(row % a.n_new);
+  const int n = packed ? cu[bi + 1] - cu[bi] : a.new_lens ? min(a.new_lens[bi], a.n_new) : a.n_new;
+  if (i < 0 || i >= n) return;  // padding
+  const long long pos = (long long)a.seq_lens[bi] - n + i;
+  int page = -1;
+  if (pos >= 0 && pos < (long long)a.max_chunks * kChunk)
+    page = a.block_table[(size_t)bi * a.max_chunks + pos / kChunk];
+  if (page < 0 || page >= a.n_pages) {
+    if (u == 0) set_error(a.err, kErrBadPage);
+    page = -1;
   }
-  __syncthreads();
-  if (a.inv_freq && h0 < a.h + a.g) {
-    for (int x = t; x < nt * nf; x += kRotThreads) {
-      const int tok = x / nf, f = x % nf;
-      if (s_tok[tok].live) s_cs[tok][f] = turn_of(s_tok[tok].pos, a.inv_freq[f]);
-    }
-    __syncthreads();
-  }
-  const int total = nh * a.tile * U;
-  for (int x0 = t; x0 < total; x0 += kRotThreads * kRotUnits) {
-    uint4 r0[kRotUnits], r1[kRotUnits];
-    T* dst[kRotUnits];
+  if (pos < 0) return;
+
+  const long long bs = packed ? 0 : bi, is = packed ? row : i;
+  const int rot = h0 < a.h + a.g ? a.rot : 0;  // a block of values needs no angles
+  Turns<E> w;
+  w.set((int)pos, a.inv_freq, u, rot, a.interleaved, false);
+  int o0, o1;
+  unit_offsets<E>(u, a.rot, a.interleaved, o0, o1);
+  const size_t cell = ((size_t)(page < 0 ? 0 : page) * a.g * kChunk + (size_t)(pos % kChunk)) * D;  // of head 0
+  // where head hh comes from and goes to
+  auto source = [&](int hh) {
+    const bool is_q = hh < a.h, is_k = !is_q && hh < a.h + a.g;
+    const Rows& R = is_q ? a.q : is_k ? a.k : a.v;
+    return static_cast<const T*>(R.data) + bs * R.batch_stride + (hh - (is_q ? 0 : is_k ? a.h : a.h + a.g)) * R.head_stride +
+           is * R.token_stride;
+  };
+  auto target = [&](int hh) {
+    if (hh < a.h)
+      return static_cast<T*>(a.q_out.data) + bs * a.q_out.batch_stride + hh * a.q_out.head_stride + is * a.q_out.token_stride;
+    const bool is_k = hh < a.h + a.g;
+    return static_cast<T*>(is_k ? a.k_pages : a.v_pages) + cell + (size_t)(hh - (is_k ? a.h : a.h + a.g)) * kChunk * D;
+  };
+  for (int h = h0; h < h1; h += kRotHeads) {
+    uint4 r0[kRotHeads], r1[kRotHeads];
 #pragma unroll
-    for (int k = 0; k < kRotUnits; ++k) {
-      const int x = x0 + k * kRotThreads;
-      const int u = x % U, tok = x / U % a.tile, hh = h0 + x / U / a.tile;
-      dst[k] = nullptr;
-      if (x < total && tok < nt) {
-        const Token& w = s_tok[tok];
-        // virtual heads: the h query heads, the g key heads, the g value heads
-        const bool is_q = hh < a.h, is_k = !is_q && hh < a.h + a.g;
-        const int head = is_q ? hh : is_k ? hh - a.h : hh - a.h - a.g;
-        if (w.live && (is_q || w.page >= 0)) {
-          const long long b_row = packed ? 0 : w.bi, i_row = packed ? row0 + tok : w.i;
-          const Rows& R = is_q ? a.q : is_k ? a.k : a.v;
-          const T* row = static_cast<const T*>(R.data) + b_row * R.batch_stride + head * R.head_stride +
-                         i_row * R.token_stride;
-          if (is_q)
-            dst[k] = static_cast<T*>(a.q_out.data) + b_row * a.q_out.batch_stride + head * a.q_out.head_stride +
-                     i_row * a.q_out.token_stride;
-          else
-            dst[k] = static_cast<T*>(is_k ? a.k_pages : a.v_pages) +
-                     (((size_t)w.page * a.g + head) * kChunk + w.pos % kChunk) * D;
-          int o0, o1;
-          unit_offsets<E>(u, is_q || is_k ? a.rot : 0, a.interleaved, o0, o1);
-          r0[k] = *reinterpret_cast<const uint4*>(row + o0);
-          r1[k] = *reinterpret_cast<const uint4*>(row + o1);
+    for (int k = 0; k < kRotHeads; ++k) {
+      if (h + k < h1) {
+        const T* p = source(h + k);
+        r0[k] = *reinterpret_cast<const uint4*>(p + o0);
+        r1[k] = *reinterpret_cast<const uint4*>(p + o1);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRotHeads; ++k) {
+      const int hh = h + k;
+      if (hh < h1 && (hh < a.h || page >= 0)) {
+        T* p = target(hh);
+        if (hh < a.h + a.g) {
+          turn_unit<T, T>(r0[k], r1[k], w, p + o0, p + o1);
+        } else {
+          *reinterpret_cast<uint4*>(p + o0) = r0[k];
+          *reinterpret_cast<uint4*>(p + o1) = r1[k];
         }
       }
-    }
-#pragma unroll
-    for (int k = 0; k < kRotUnits; ++k) {
-      const int x = x0 + k * kRotThreads;
-      const int u = x % U, tok = x / U % a.tile, hh = h0 + x / U / a.tile;
-      if (dst[k]) turn_unit<T, T>(r0[k], r1[k], u, hh < a.h + a.g ? a.rot : 0, a.interleaved, s_cs[tok], dst[k]);
     }
   }
 }
 
-cudaError_t run_append(AppendArgs a, cudaStream_t st) {
-  const bool packed = a.cu_new != nullptr;
+template <typename T, int D>
+static cudaError_t launch_append(AppendArgs a, cudaStream_t st) {
+  constexpr int kRows = kRotThreads / (D / (2 * Unit<T>::E));
   const int heads = a.h + 2 * a.g;
-  const long long tokens = packed ? a.n_new : (long long)a.b * a.n_new;
-  long long n_work = 0, n_tile = 0;
-  if (tokens > 0) {
-    pick_tile(tokens, heads, &a.tile, &a.head_block);
-    n_tile = (a.n_new + a.tile - 1) / a.tile;
-    n_work = n_tile * (packed ? 1 : a.b) * ((heads + a.head_block - 1) / a.head_block);
-  }
+  const long long tokens = a.cu_new ? a.n_new : (long long)a.b * a.n_new;
+  const long long token_blocks = (tokens + kRows - 1) / kRows;
+  a.head_block = pick_heads(token_blocks, heads);
+  const long long n_work = token_blocks * ((heads + a.head_block - 1) / a.head_block);
   const long long blocks = n_work + (a.n_slots + kRotThreads - 1) / kRotThreads;
   if (blocks == 0) return cudaSuccess;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  if (a.bf16) {
-    if (a.d == 64) append_kernel<__nv_bfloat16, 64><<<(unsigned)blocks, kRotThreads, 0, st>>>(a, (int)n_work, (int)n_tile);
-    else append_kernel<__nv_bfloat16, 128><<<(unsigned)blocks, kRotThreads, 0, st>>>(a, (int)n_work, (int)n_tile);
-  } else {
-    if (a.d == 64) append_kernel<float, 64><<<(unsigned)blocks, kRotThreads, 0, st>>>(a, (int)n_work, (int)n_tile);
-    else append_kernel<float, 128><<<(unsigned)blocks, kRotThreads, 0, st>>>(a, (int)n_work, (int)n_tile);
-  }
+  append_kernel<T, D><<<(unsigned)blocks, kRotThreads, 0, st>>>(a, (int)n_work);
   return cudaGetLastError();
+}
+
+cudaError_t run_append(const AppendArgs& a, cudaStream_t st) {
+  if (a.bf16) return a.d == 64 ? launch_append<__nv_bfloat16, 64>(a, st) : launch_append<__nv_bfloat16, 128>(a, st);
+  return a.d == 64 ? launch_append<float, 64>(a, st) : launch_append<float, 128>(a, st);
 }
 
 }  // namespace hils

@@ -380,8 +380,10 @@ HILS_API hils_status hils_decode_ex(const hils_shape* shape, const void* q, cons
 
 /* Rows of head_dim adjacent elements, one per (batch, head, token):
  * row = data + batch*batch_stride + head*head_stride + token*token_stride, strides in
- * elements.  data and every stride times the element size are multiples of 16 bytes, so
- * slices of a fused [tokens, (h + 2g) * d] projection are read where they lie. */
+ * elements, not negative (a dimension of one entry needs none).  data and every stride times the element size are multiples of
+ * 16 bytes, so slices of a fused [tokens, (h + 2g) * d] projection are read where they lie.
+ * Rows that are written share no element with one another, and lie apart from every other
+ * tensor of the call but, where this is said, their own input. */
 typedef struct {
   void* data;
   int64_t batch_stride, head_stride, token_stride;
@@ -412,8 +414,8 @@ typedef struct {
  *   positions    NULL: token i is at position i; else int32 [seq_len], or
  *                [batch, seq_len] with position_stride = seq_len (0: shared by the batch)
  *   out_dtype    hils_dtype of q_out and k_out
- * An output may be its input's own memory (same data, strides and type); any other overlap
- * is an error of the caller.
+ * An output may be its input's own memory (same data, strides and type; the other tensor may
+ * then lie between its rows, as slices of one fused tensor do); any other overlap is refused.
  */
 HILS_API hils_status hils_rotate(const hils_shape* shape, const hils_rows* q, const hils_rows* k,
                                  const hils_rope* rope, const int32_t* positions, int64_t position_stride,
@@ -427,7 +429,7 @@ HILS_API hils_status hils_rotate(const hils_shape* shape, const hils_rows* q, co
  *   shape        batch, heads_q, heads_kv, head_dim, chunk and dtype (of every tensor) are
  *                read; the other fields must be valid
  *   k, v         rows of heads_kv heads: the new tokens
- *   q, q_out     rows of heads_q heads, or both NULL
+ *   q, q_out     rows of heads_q heads, or both NULL; q_out may be q's own memory
  *   n_new        cu_new == NULL: tokens per sequence of the rows' batch dimension
  *                (token i of sequence b is row (b, head, i)); new_lens [batch] int32 may
  *                shorten sequence b to its first new_lens[b] tokens (NULL: all n_new).

@@ -76,7 +76,7 @@ def test_rotate_arguments():
     dict(positions=torch.zeros(2 * N, dtype=torch.int32)[::2]),
     dict(q_out=torch.zeros(B, H, N, D, dtype=torch.float16)),
     dict(q_out=torch.zeros(B, H, N + 1, D, dtype=BF)),
-    dict(q_out=torch.zeros(B, N, H, D, dtype=BF).transpose(1, 2)),
+    dict(q_out=torch.zeros(B, H, D, N, dtype=BF).transpose(2, 3)),
     dict(k_out=torch.zeros(B, G, N, D, dtype=BF)),
     dict(inv_freq=None),
 ])
@@ -88,40 +88,43 @@ def test_rotate_refuses(kw):
 
 
 def test_rotate_refuses_overlapping_and_expanded_outputs():
-    f = torch.ones(16)
-    buf = torch.zeros(2 * B * H * N * D, dtype=BF)
-    q = buf[:B * H * N * D].view(B, H, N, D)
-    with pytest.raises(ValueError):  # shifted by one row
-        check_rotate_args(q, f, q_out=buf[D:D + B * H * N * D].view(B, H, N, D))
-    with pytest.raises(ValueError):  # one memory for every head, in place
-        x = torch.zeros(B, 1, N, D, dtype=BF).expand(B, H, N, D)
-        check_rotate_args(x, f, q_out=x)
-    k = torch.zeros(B, G, N, D, dtype=BF)
-    with pytest.raises(ValueError):  # k_out on q
-        check_rotate_args(q, f, k, k_out=q.view(-1)[:B * G * N * D].view(B, G, N, D))
-    with pytest.raises(ValueError):  # q_out on k
-        kk = buf[:B * G * N * D].view(B, G, N, D)
-        check_rotate_args(torch.zeros(B, H, N, D, dtype=BF), f, kk, q_out=q)
+    """By hils_rotate, before anything is launched: addresses are compared, not read."""
+    L, ref = hils.lib(), ctypes.byref
+    s, ro = _sh(seq_len=70), Rope(1 << 20, 32, 0)  # q [2, 8, 70, 64], k [2, 2, 70, 64] bf16
+    base, qn = 1 << 20, 2 * 8 * 70 * 64
+    dense = lambda p, h: Rows(p, h * 70 * 64, 70 * 64, 64)
+    q, k = dense(base, 8), dense(base + (1 << 24), 2)
+    qo, ko = dense(base + (2 << 24), 8), dense(base + (3 << 24), 2)
+
+    def call(q=q, k=k, qo=qo, ko=ko, od=1):
+        return L.hils_rotate(ref(s), ref(q), ref(k), ref(ro), None, 0, 0, ref(qo), ref(ko), od, None)
+
+    assert call(qo=dense(base + 128, 8)) == 1                     # shifted by one row
+    assert call(qo=dense(base + 2 * qn - 16, 8)) == 1             # its end
+    assert call(qo=dense(k.data, 8)) == 1                         # on the other input
+    assert call(ko=dense(qo.data, 2)) == 1                        # on the other output
+    assert call(ko=dense(base, 2)) == 1                           # k_out on q
+    assert call(qo=q, od=0) == 1                                  # in place with another type
+    expanded = Rows(base, 70 * 64, 0, 64)
+    assert call(q=expanded, qo=expanded) == 1                     # one memory for every head, in place
+    assert call(qo=Rows(qo.data, 8 * 70 * 64, 70 * 64, 56)) == 1  # rows that share elements
+    assert call(qo=Rows(qo.data, 0, 70 * 64, 64)) == 1
+    assert call(q=Rows(base, -64, 70 * 64, 64)) == 1
 
 
 @pytest.mark.parametrize("f", [torch.ones(0), torch.ones(4), torch.ones(40), torch.ones(16, dtype=torch.float64),
                                torch.ones(4, 4), torch.ones(32)[::2]])
 def test_rope_refuses(f):
     with pytest.raises((ValueError, TypeError)):
-        _abi._rope(f, False, 64)
+        _abi._rope_words(f, False, 64)
 
 
-def test_rows_need_aligned_contiguous_rows():
-    x = torch.zeros(2, 3, 5, 72, dtype=BF)
-    assert _abi._rows(x[..., :64], "x").token_stride == 72
+def test_rows_need_contiguous_last_dimension():
+    x = torch.zeros(2, 3, 64, 8, dtype=BF).transpose(2, 3)
     with pytest.raises(ValueError):
-        _abi._rows(x[..., 4:68], "x")
+        check_rotate_args(x, torch.ones(16))
     with pytest.raises(ValueError):
-        _abi._rows(torch.zeros(2, 3, 5, 68, dtype=BF)[..., :64], "x")
-    with pytest.raises(ValueError):
-        _abi._rows(torch.zeros(2, 3, 64, 8, dtype=BF).transpose(2, 3), "x")
-    # the stride of a single entry is not looked at
-    assert _abi._rows(torch.zeros(1, 3, 1, 64, dtype=BF).as_strided((1, 3, 1, 64), (7, 64, 5, 1)), "x").batch_stride == 0
+        check_rotate_args(torch.zeros(2, 3, 8, 64, dtype=BF), torch.ones(16), q_out=x)
 
 
 def _append_args(dtype=BF, **kw):
@@ -242,9 +245,17 @@ def test_append_rejects_before_launch():
     assert call(n=-1) == 1 and call(cu=FAKE, nl=FAKE) == 1 and call(sl=None) == 1 and call(bt=None) == 1
     assert call(mc=0) == 1 and call(np_=0) == 1 and call(kp=None) == 1 and call(vp=P_((1 << 20) + 4)) == 1
     assert call(k=Rows(1 << 20, 64, 4, 64)) == 1
+    far = lambda i, h: Rows((i + 1) << 28, h * 4 * 64, 4 * 64, 64)
+    good = dict(k=far(0, 2), v=far(1, 2), q=far(2, 8), qo=far(3, 8), kp=P_(5 << 28), vp=P_(6 << 28))
+    assert call(**good, ws=None) == 3                                # nothing else is wrong with it
+    assert call(**{**good, "vp": P_((5 << 28) + 16)}) == 1           # the pools overlap
+    assert call(**{**good, "k": far(4, 2)}) == 1                     # keys read from the pool
+    assert call(**{**good, "qo": far(0, 8)}) == 1                    # queries written over the keys
+    assert call(**{**good, "qo": far(2, 8)}, ws=None) == 3           # in place
+    assert call(**{**good, "qo": Rows(4 << 28, 4 * 64, 0, 64)}) == 1  # one row for every head
     assert call(rope=Rope(1 << 20, 24, 0)) == 2 and call(mc=1 << 26) == 2
     assert call(n=(1 << 31) - 1) == 2  # more rows than 32 bits count
-    assert call(ws=None) == 3 and call(wsb=128) == 3
+    assert call(**good, wsb=128) == 3
     assert call(s=_sh(batch=0)) == 0 and call(n=0, k=None, v=None, q=None, qo=None, ws=None) == 0
     n = ctypes.c_size_t(0)
     assert L.hils_workspace_size(ref(s), hils.OP_APPEND, ref(n)) == 0 and n.value >= 256

@@ -91,6 +91,18 @@ def test_rotate_matches_oracle(dtype, out_dtype, d, rot, inter, b, h, g, n, pos)
             _close(o, want, _rotate_bound(_np(x), want, od, rot, inter), "rotate")
 
 
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotate_copies_what_lies_behind_the_rotated_part(inter):
+    """Bit for bit, whatever it is (an infinity beside a number among it)."""
+    for dt in DT.values():
+        x = _randn(1, 2, 40, 64, dtype=dt, seed=8)
+        x[..., 33::2], x[0, 0, 5, 40], x[0, 1, 7, 50] = -math.inf, math.nan, -0.0
+        y = hils.rotate(x, _freq(32), interleaved=inter)
+        bits = torch.int16 if dt == torch.bfloat16 else torch.int32
+        assert torch.equal(y[..., 32:].view(bits), x[..., 32:].view(bits))
+        assert torch.isfinite(y[..., :32]).all()
+
+
 def test_rotate_in_place_and_alone():
     q = _randn(2, 4, 130, 64, dtype=torch.bfloat16, seed=0)
     f = _freq(64)
