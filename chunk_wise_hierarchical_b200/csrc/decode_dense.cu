@@ -8,19 +8,23 @@
 // beyond the CUDA cores -- so the bf16 products run on the tensor cores with the keys as the
 // M = 16 rows and the heads as the N = 8 columns of mma.m16n8k16.
 //
-// Split.  The tiles (kDenseTile keys of one (sequence, KV head), "units") of the whole batch
-// are numbered in a row, and CTA i of kDenseCtas takes units [i per, (i + 1) per): every SM
-// reads the same number of bytes whatever the lengths are, and the host needs none of them
-// (the launch is the same for every step, so a graph can hold it).  A (sequence, KV head)
-// whose units all lie in one CTA is written by it.  One that is cut leaves partials (max,
-// sum, unnormalised output) in the workspace, at most two per CTA; the CTA that takes the
-// last ticket joins them in CTA order, so that the result does not depend on who that is.
-// No CTA waits for another.
+// Split.  The tiles (kTile keys of one (sequence, KV head), "units") of the whole batch are
+// numbered in a row, and CTA i of kDenseCtas takes units [i per, (i + 1) per): every SM reads
+// the same number of bytes whatever the lengths are, and the host needs none of them (the
+// launch is the same for every step, so a graph can hold it).  A (sequence, KV head) whose
+// units all lie in one CTA is written by it.  One that is cut leaves partials (max, sum,
+// unnormalised output) in the workspace, at most two per CTA; the CTA that takes the last
+// ticket joins them in CTA order, so that the result does not depend on who that is.  No CTA
+// waits for another.
 //
-// Within a CTA one warp reads the block table, 32 units at a time, and feeds a ring of stages
-// by TMA (K and V tile of a unit, 128-byte swizzle).  kDenseWarps consumer warps take 16 keys
-// of a tile each; they do not wait for one another inside a (sequence, KV head): each keeps its
-// own running maximum, sum and output, and the warps are joined in shared memory at its end.
+// Within a CTA, the kTileWarps warps of group j take units j, j + kGroups, ... and feed
+// themselves: they read their part of the block table 32 units at a time, and a lane of the
+// group's first warp refills a stage of the group's own ring by TMA (K and V tile, 128-byte
+// swizzle) as soon as the group has consumed it.  Nobody else is waited for: each warp keeps its
+// own running maximum, sum and output, and the warps are joined in shared memory at the end of
+// each (sequence, KV head).  (One producer warp feeding all through full and empty barriers was
+// tried first: its loop took about 500 cycles a unit, which 16 KB units -- 700 cycles of the SM's
+// share of HBM -- do not hide.)
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -35,36 +39,35 @@ namespace hils {
 
 namespace {
 
-constexpr int kDenseWarps = 8;                      // consumer warps
-constexpr int kDenseThreads = (kDenseWarps + 1) * 32;
-constexpr int kDenseCtas = 148;                     // one per SM
-constexpr int kDenseSeqs = 1024;                    // sequences of one launch (their prefix sums in shared memory)
-constexpr int kDenseStatic = 10 * 1024;             // room left for the static shared variables
+constexpr int kDenseWarps = 8;
+constexpr int kDenseThreads = kDenseWarps * 32;
+constexpr int kDenseCtas = 148;          // one per SM
+constexpr int kDenseSeqs = 1024;         // sequences of one launch (their prefix sums in shared memory)
+constexpr int kDenseRing = 128 * 1024;   // bytes of the rings of a CTA
+constexpr int kDenseMaxTiles = 2;        // units of a chunk and KV head, at most
+constexpr int kDenseMinUnits = 2;        // units of a CTA, at least
 
 // T element, D head dim, G heads per KV head.
 template <typename T, int D, int G>
 struct DenseCfg {
   static constexpr int kTile = sizeof(T) == 2 ? 64 : 32;         // keys per unit
+  static constexpr int kTileWarps = 2;                           // warps that share a unit
+  static constexpr int kSlice = kTile / kTileWarps;              // keys of it that one warp takes
+  static constexpr int kGroups = kDenseWarps / kTileWarps;
   static constexpr int kCols = 128 / (int)sizeof(T);             // columns of a swizzled sub-tile
   static constexpr int kSubs = D / kCols;
   static constexpr uint32_t kSub = kTile * 128u;                 // bytes of a sub-tile
   static constexpr uint32_t kHalf = kSubs * kSub;                // K (or V) of a stage
   static constexpr uint32_t kStage = 2 * kHalf;
-  static constexpr int kTileWarps = kTile / 16;                  // consumer warps of one unit
-  static constexpr int kGroups = kDenseWarps / kTileWarps;       // units in flight among the consumers
+  static constexpr int kStages = kDenseRing / kGroups / (int)kStage;  // of a group
   static constexpr int kVec = G * D / 4;                         // float4 columns of an output
-  // shared memory behind the ring, in floats
+  // shared memory behind the rings, in floats
   static constexpr int kJoin = kDenseWarps * G * D > 2560 ? kDenseWarps * G * D : 2560;
   static constexpr int kQ = sizeof(T) == 4 ? G * D : 0;
   static constexpr int kP = sizeof(T) == 4 ? kDenseWarps * 16 * G : 0;
-  // Stages: what fits, in a multiple of kGroups.  Stage s then serves the same group in every
-  // round, and a warp sees each phase of the barriers it waits on; with another number a warp
-  // could meet a stage two fills later, where the parity of the phase it waits for is that of
-  // one long complete.
-  static constexpr int kStages =
-      (227 * 1024 - 1024 - kDenseStatic - 4 * (kJoin + kQ + kP)) / (int)kStage / kGroups * kGroups;
-  static_assert(kStages >= kGroups && kStages % kGroups == 0, "a stage belongs to one group of warps");
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + 4ull * (kJoin + kQ + kP);
+  static constexpr uint32_t kRings = kGroups * kStages * kStage;
+  static constexpr size_t kSmem = 1024 + (size_t)kRings + 4ull * (kJoin + kQ + kP);
+  static_assert(kStages >= 1 && kSmem <= 227 * 1024 - 10 * 1024, "room for the static shared variables");
 };
 
 struct alignas(64) DenseKernelArgs {
@@ -75,11 +78,6 @@ struct alignas(64) DenseKernelArgs {
   unsigned* ticket;            // [b g], zero between calls
 };
 
-__device__ __forceinline__ void bar_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(kDenseWarps * 32) : "memory"); }
-
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -121,11 +119,11 @@ __device__ __forceinline__ float raise_max(float& m, float t, float& base) {
   return c;
 }
 
-// bf16: the warp's state over its 16-key slices.  Lane l holds heads 2 (l % 4), + 1, as the
+// bf16: the warp's state over its slices of 16 NS keys.  Lane l holds heads 2 (l % 4), + 1, as the
 // columns of the transposed score tile S^T = K Q^T and of O^T = V^T P^T.  P is split into
 // bf16 hi + lo parts (two products), so that its rounding (2^-17) stays below that of the
 // output; the tensor cores have the room at this byte rate.
-template <int D, int G>
+template <int D, int G, int NS>
 struct WarpStateBf16 {
   float m[2], l[2], o[D / 16][4];
   uint32_t q[D / 16][2];
@@ -144,22 +142,34 @@ struct WarpStateBf16 {
     l[0] = l[1] = 0.f;
   }
 
-  // Keys [row0, row0 + 16) of a tile with `valid` keys (row0 < valid).
+  // Keys [row0, row0 + 16 NS) of a tile with `valid` keys (> row0): NS 16-key products side by
+  // side, one step of the running maximum for all.
   __device__ void consume(uint32_t sk, uint32_t sv, int row0, int valid, float scale, const float*, float*, int lane) {
-    constexpr uint32_t kSub = 64 * 128;
-    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // two chains of products
+    constexpr uint32_t kSub = DenseCfg<__nv_bfloat16, D, G>::kSub;
+    float s[NS][4];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      uint32_t f[4];
-      ldsm4(sk + (k >> 2) * kSub + tc::sw128_chunk(row0 + (lane & 15), (k & 3) * 2 + (lane >> 4)), f);
-      mma16816(s[k & 1], f, q[k][0], q[k][1]);
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        uint32_t f[4];
+        ldsm4(sk + (k >> 2) * kSub + tc::sw128_chunk(row0 + 16 * i + (lane & 15), (k & 3) * 2 + (lane >> 4)), f);
+        mma16816(s[i], f, q[k][0], q[k][1]);
+      }
     }
-    const int r0 = row0 + (lane >> 2), r1 = r0 + 8;
-    const float x0 = r0 < valid ? (s[0][0] + s[1][0]) * scale : -INFINITY;
-    const float x1 = r0 < valid ? (s[0][1] + s[1][1]) * scale : -INFINITY;
-    const float x2 = r1 < valid ? (s[0][2] + s[1][2]) * scale : -INFINITY;
-    const float x3 = r1 < valid ? (s[0][3] + s[1][3]) * scale : -INFINITY;
-    float t0 = fmaxf(x0, x2), t1 = fmaxf(x1, x3);
+    // s[i]: keys r, r (heads 2c, 2c + 1), r + 8, r + 8, r = row0 + 16 i + lane / 4
+    float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const bool ok = row0 + 16 * i + 8 * e + (lane >> 2) < valid;
+        s[i][2 * e] = ok ? s[i][2 * e] * scale : -INFINITY;
+        s[i][2 * e + 1] = ok ? s[i][2 * e + 1] * scale : -INFINITY;
+        t0 = fmaxf(t0, s[i][2 * e]);
+        t1 = fmaxf(t1, s[i][2 * e + 1]);
+      }
 #pragma unroll
     for (int d = 4; d < 32; d <<= 1) {
       t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, d));
@@ -167,34 +177,44 @@ struct WarpStateBf16 {
     }
     float b0, b1;
     const float c0 = raise_max(m[0], t0, b0), c1 = raise_max(m[1], t1, b1);
-    const float p0 = exp2f(x0 - b0), p1 = exp2f(x1 - b1), p2 = exp2f(x2 - b0), p3 = exp2f(x3 - b1);
-    l[0] = l[0] * c0 + (p0 + p2);
-    l[1] = l[1] * c1 + (p1 + p3);
+    l[0] *= c0;
+    l[1] *= c1;
     if (__any_sync(0xffffffffu, c0 != 1.f || c1 != 1.f)) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         o[k][0] *= c0; o[k][1] *= c1; o[k][2] *= c0; o[k][3] *= c1;
       }
     }
-    const uint32_t h01 = tc::pack_bf16x2(p0, p1), h23 = tc::pack_bf16x2(p2, p3);
-    const uint32_t l01 = tc::pack_bf16x2(p0 - __uint_as_float(h01 << 16), p1 - __uint_as_float(h01 & 0xffff0000u));
-    const uint32_t l23 = tc::pack_bf16x2(p2 - __uint_as_float(h23 << 16), p3 - __uint_as_float(h23 & 0xffff0000u));
-    const uint32_t ph0 = transpose8(h01), ph1 = transpose8(h23), pl0 = transpose8(l01), pl1 = transpose8(l23);
-    // values behind the last key may be anything: they are cleared, not only weighted by 0
-    const int k0 = row0 + (lane & 3) * 2;
-    const bool tail = row0 + 16 > valid;
-    const uint32_t keep0 = (k0 < valid ? 0xffffu : 0u) | (k0 + 1 < valid ? 0xffff0000u : 0u);
-    const uint32_t keep1 = (k0 + 8 < valid ? 0xffffu : 0u) | (k0 + 9 < valid ? 0xffff0000u : 0u);
+    // P^T as the second operand: bf16 hi and lo parts of keys (0-7, 8-15) of each slice
+    uint32_t ph[NS][2], pl[NS][2], keep[NS][2];
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float p0 = exp2f(s[i][2 * e] - b0), p1 = exp2f(s[i][2 * e + 1] - b1);
+        l[0] += p0;
+        l[1] += p1;
+        const uint32_t h = tc::pack_bf16x2(p0, p1);
+        ph[i][e] = transpose8(h);
+        pl[i][e] = transpose8(tc::pack_bf16x2(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u)));
+        // values behind the last key may be anything: they are cleared, not only weighted by 0
+        const int k0 = row0 + 16 * i + 8 * e + (lane & 3) * 2;
+        keep[i][e] = (k0 < valid ? 0xffffu : 0u) | (k0 + 1 < valid ? 0xffff0000u : 0u);
+      }
+    const bool tail = row0 + 16 * NS > valid;
     const uint32_t vrow = row0 + (lane & 7) + ((lane >> 4) << 3), vch = (lane >> 3) & 1;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      uint32_t f[4];
-      ldsm4_t(sv + (k >> 2) * kSub + tc::sw128_chunk(vrow, (k & 3) * 2 + vch), f);
-      if (tail) {
-        f[0] &= keep0; f[1] &= keep0; f[2] &= keep1; f[3] &= keep1;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        uint32_t f[4];
+        ldsm4_t(sv + (k >> 2) * kSub + tc::sw128_chunk(vrow + 16 * i, (k & 3) * 2 + vch), f);
+        if (tail) {
+          f[0] &= keep[i][0]; f[1] &= keep[i][0]; f[2] &= keep[i][1]; f[3] &= keep[i][1];
+        }
+        mma16816(o[k], f, ph[i][0], ph[i][1]);
+        mma16816(o[k], f, pl[i][0], pl[i][1]);
       }
-      mma16816(o[k], f, ph0, ph1);
-      mma16816(o[k], f, pl0, pl1);
     }
   }
 
@@ -233,8 +253,8 @@ struct WarpStateF32 {
 
   __device__ void start(const DenseArgs& a, int bi, int gi, float* sq, int, int ct) {
     const float* row = static_cast<const float*>(a.q) + ((size_t)bi * a.h + gi * G) * D;
-    for (int x = ct; x < G * D; x += kDenseWarps * 32) sq[x] = __ldg(row + x);
-    bar_consumers();
+    for (int x = ct; x < G * D; x += kDenseThreads) sq[x] = __ldg(row + x);
+    __syncthreads();
 #pragma unroll
     for (int hh = 0; hh < G; ++hh) {
       m[hh] = -INFINITY;
@@ -244,9 +264,10 @@ struct WarpStateF32 {
     }
   }
 
+  // Keys [row0, row0 + 16) of a tile with `valid` keys (> row0).
   __device__ void consume(uint32_t sk, uint32_t sv, int row0, int valid, float scale, const float* sq, float* sp,
                           int lane) {
-    constexpr uint32_t kSub = 32 * 128;
+    constexpr uint32_t kSub = DenseCfg<float, D, G>::kSub;
     const int rr = lane >> 2, c = lane & 3;
     const int pr = ((rr & 1) << 2) | (rr >> 1);
     float sa[G], sb[G];
@@ -326,7 +347,8 @@ struct WarpStateF32 {
 };
 
 template <typename T, int D, int G> struct WarpState;
-template <int D, int G> struct WarpState<__nv_bfloat16, D, G> : WarpStateBf16<D, G> {};
+template <int D, int G>
+struct WarpState<__nv_bfloat16, D, G> : WarpStateBf16<D, G, DenseCfg<__nv_bfloat16, D, G>::kSlice / 16> {};
 template <int D, int G> struct WarpState<float, D, G> : WarpStateF32<D, G> {};
 
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
@@ -361,36 +383,37 @@ __device__ __forceinline__ int seq_of(const unsigned* prefix, int n, unsigned u)
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __grid_constant__ DenseKernelArgs ka) {
   using C = DenseCfg<T, D, G>;
-  constexpr int kConsumers = kDenseWarps * 32;
   extern __shared__ unsigned char smem_raw[];
   __shared__ unsigned s_prefix[kDenseSeqs + 1];  // units before each sequence
   __shared__ int s_len[kDenseSeqs];
-  __shared__ unsigned s_scan[kDenseWarps];
-  __shared__ uint64_t s_full[C::kStages], s_empty[C::kStages];
-  __shared__ int s_bad[C::kStages];               // the stage's page id was out of range
+  __shared__ __align__(16) unsigned s_scan[kDenseWarps];
+  __shared__ uint64_t s_full[C::kGroups][C::kStages];
   __shared__ float s_m[kDenseWarps][G], s_l[kDenseWarps][G], s_M[G], s_z[G];
   __shared__ int s_abort, s_last;
 
   const DenseArgs& a = ka.a;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const uint32_t ring = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
-  float* s_join = reinterpret_cast<float*>(smem_raw + (ring - tc::smem_u32(smem_raw)) + (size_t)C::kStages * C::kStage);
+  const uint32_t ring0 = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int group = warp / C::kTileWarps, row0 = warp % C::kTileWarps * C::kSlice;
+  const bool feeds = warp % C::kTileWarps == 0;  // the group's first warp issues its copies
+  const uint32_t ring = ring0 + group * C::kStages * C::kStage;
+  float* s_join = reinterpret_cast<float*>(smem_raw + (ring0 - tc::smem_u32(smem_raw)) + C::kRings);
   float* s_q = s_join + C::kJoin;
-  float* s_p = s_q + C::kQ;
+  float* s_p = s_q + C::kQ + warp * 16 * G;
 
-  if (t == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      tc::mbar_init(tc::smem_u32(&s_full[s]), 1);
-      tc::mbar_init(tc::smem_u32(&s_empty[s]), C::kTileWarps);
-    }
+  if (feeds && lane == 0) {
+    for (int s = 0; s < C::kStages; ++s) tc::mbar_init(tc::smem_u32(&s_full[group][s]), 1);
     tc::mbar_fence_init();
+  }
+  if (t == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&ka.tmap_k) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&ka.tmap_v) : "memory");
     s_abort = 0;
     s_prefix[0] = 0;
   }
-  // units before each sequence: thread t < 256 counts sequences 4 t .. 4 t + 3
-  constexpr int kPer = kDenseSeqs / kConsumers;
-  unsigned mine[kPer], sum = 0;
-  if (t < kConsumers) {
+  {  // units before each sequence: thread t counts sequences 4 t .. 4 t + 3
+    constexpr int kPer = kDenseSeqs / kDenseThreads;
+    unsigned mine[kPer], sum = 0;
     const long long cap = (long long)a.max_chunks * kChunk;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -412,91 +435,78 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
     }
     if (lane == 31) s_scan[warp] = inc;
     sum = inc - sum;  // before this thread, within the warp
-  }
-  __syncthreads();
-  if (t < kConsumers) {
-    for (int w = 0; w < warp; ++w) sum += s_scan[w];
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kDenseWarps; ++w) sum += w < warp ? s_scan[w] : 0u;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) s_prefix[t * kPer + i + 1] = sum + mine[i];
   }
   __syncthreads();
   const unsigned total = s_prefix[a.b];
-  const unsigned per = (total + kDenseCtas - 1) / kDenseCtas;
+  const unsigned per = max((unsigned)kDenseMinUnits, (total + kDenseCtas - 1) / kDenseCtas);
   const unsigned u0 = min(total, blockIdx.x * per), u1 = min(total, u0 + per);
 
-  if (warp == kDenseWarps) {
-    // ---- producer: lane i finds the page of unit base + i, lane 0 issues the copies ----
-    auto locate = [&](unsigned u, int& y, int& z) {
-      z = -1;
-      y = 0;
-      if (u >= u1) return;
-      const int b = seq_of(s_prefix, a.b, u);
-      const int L = s_len[b];
-      const int nt = n_tiles<C::kTile>(L, a.n_win);
-      const int rem = (int)(u - s_prefix[b]);
-      const int tile = first_tile<C::kTile>(L, a.n_win) + rem % nt;
-      const int page = a.block_table[(size_t)b * a.max_chunks + tile * C::kTile / kChunk];
-      y = tile * C::kTile % kChunk;
-      if (page >= 0 && page < a.n_pages) z = page * a.g + rem / nt;
-      else set_error(a.err, kErrBadPage);
-    };
-    int y, z;
-    locate(u0 + lane, y, z);
-    bool alive = true;
-    unsigned done = u0;
-    for (unsigned base = u0; base < u1 && alive; base += 32) {
-      int yn, zn;
-      locate(base + 32 + lane, yn, zn);
-      for (int i = 0; i < 32 && base + i < u1; ++i) {
-        const int yi = __shfl_sync(0xffffffffu, y, i), zi = __shfl_sync(0xffffffffu, z, i);
-        const unsigned n = base + i - u0;
-        const int st = (int)(n % C::kStages);
-        const unsigned round = n / C::kStages;
-        if (lane == 0) {
-          if (round > 0 && !tc::mbar_wait(tc::smem_u32(&s_empty[st]), (round & 1) ^ 1, a.poll)) alive = false;
-          if (alive) {
-            const uint32_t full = tc::smem_u32(&s_full[st]), dst = ring + st * C::kStage;
-            s_bad[st] = zi < 0;
-            if (zi < 0) {
-              mbar_arrive(full);
-            } else {
-              tc::mbar_arrive_expect_tx(full, C::kStage);
-#pragma unroll
-              for (int s = 0; s < C::kSubs; ++s) {
-                tc::tma_load_3d(dst + s * C::kSub, &ka.tmap_k, s * C::kCols, yi, zi, full);
-                tc::tma_load_3d(dst + C::kHalf + s * C::kSub, &ka.tmap_v, s * C::kCols, yi, zi, full);
-              }
-            }
-          }
-        }
-        alive = __shfl_sync(0xffffffffu, (int)alive, 0);
-        if (!alive) break;
-        done = base + i + 1;
-      }
+  // The group's units: number i is unit u0 + group + kGroups i.  Lane j knows the place of number
+  // base + j (z: block of the pool, -1 for a bad page; y: row in it) and of the 32 after those.
+  auto locate = [&](unsigned i, int& y, int& z) {
+    const unsigned u = u0 + group + i * C::kGroups;
+    z = -1;
+    y = 0;
+    if (u >= u1) return;
+    const int b = seq_of(s_prefix, a.b, u);
+    const int L = s_len[b];
+    const int nt = n_tiles<C::kTile>(L, a.n_win);
+    const int rem = (int)(u - s_prefix[b]);
+    const int tile = first_tile<C::kTile>(L, a.n_win) + rem % nt;
+    const int page = a.block_table[(size_t)b * a.max_chunks + tile * C::kTile / kChunk];
+    y = tile * C::kTile % kChunk;
+    if (page >= 0 && page < a.n_pages) z = page * a.g + rem / nt;
+    else set_error(a.err, kErrBadPage);
+  };
+  const unsigned mine = u0 + group < u1 ? (u1 - u0 - group + C::kGroups - 1) / C::kGroups : 0;
+  unsigned issued = 0, base = 0, bad = 0;  // bad: bit s, stage s has no page
+  int y, z, yn = 0, zn = -1;
+  locate(lane, y, z);
+  if (mine > 32) locate(32 + lane, yn, zn);
+  auto issue = [&]() {  // the next unit's copies (every lane of the group calls it)
+    if (issued - base == 32) {
+      base += 32;
       y = yn;
       z = zn;
+      if (base + 32 < mine) locate(base + 32 + lane, yn, zn);
     }
-    if (lane == 0) {
-      if (!alive) set_error(a.err, kErrTimeout);
-      // the copies in flight land before the CTA can end
-      const unsigned n = done - u0;
-      for (unsigned k = n > (unsigned)C::kStages ? n - C::kStages : 0; k < n; ++k)
-        tc::mbar_wait(tc::smem_u32(&s_full[k % C::kStages]), (k / C::kStages) & 1, kDrainPolls);
+    const int yi = __shfl_sync(0xffffffffu, y, issued - base), zi = __shfl_sync(0xffffffffu, z, issued - base);
+    const int st = (int)(issued % C::kStages);
+    bad = zi < 0 ? bad | 1u << st : bad & ~(1u << st);
+    if (feeds && lane == 0 && zi >= 0) {
+      const uint32_t full = tc::smem_u32(&s_full[group][st]), dst = ring + st * C::kStage;
+      tc::fence_async_smem();  // the stage's last reads, before the copies into it
+      tc::mbar_arrive_expect_tx(full, C::kStage);
+#pragma unroll
+      for (int s = 0; s < C::kSubs; ++s) {
+        tc::tma_load_3d(dst + s * C::kSub, &ka.tmap_k, s * C::kCols, yi, zi, full);
+        tc::tma_load_3d(dst + C::kHalf + s * C::kSub, &ka.tmap_v, s * C::kCols, yi, zi, full);
+      }
     }
-    return;
-  }
+    ++issued;
+  };
+  while (issued < mine && issued < (unsigned)C::kStages) issue();
+  unsigned phases = 0;  // bit s: parity of the next fill of stage s to wait for
 
-  // ---- consumers ----
+  auto group_sync = [&]() {
+    if constexpr (C::kTileWarps == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(C::kTileWarps * 32) : "memory");
+  };
+
   T* out = static_cast<T*>(a.out);
   // sequences without keys
   for (int b = blockIdx.x; b < a.b; b += kDenseCtas) {
     if (s_len[b] > 0) continue;
-    for (int x = t; x < a.h * D / 4; x += kConsumers)
+    for (int x = t; x < a.h * D / 4; x += kDenseThreads)
       store4(out + (size_t)b * a.h * D + x * 4, make_float4(0.f, 0.f, 0.f, 0.f));
     if (a.lse)
-      for (int x = t; x < a.h; x += kConsumers) a.lse[(size_t)b * a.h + x] = -INFINITY;
+      for (int x = t; x < a.h; x += kDenseThreads) a.lse[(size_t)b * a.h + x] = -INFINITY;
   }
-  const int group = warp / C::kTileWarps, row0 = (warp % C::kTileWarps) * 16;
   const float scale = a.scale * 1.4426950408889634f;  // logits in units of log 2
   bool failed = false;
 
@@ -511,6 +521,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
   };
 
   int bi = u0 < u1 ? seq_of(s_prefix, a.b, u0) : 0;
+  unsigned i = 0, stuck = 0;  // the group's next unit; the one this warp gave up at
   for (unsigned u = u0; u < u1;) {
     while (s_prefix[bi + 1] <= u) ++bi;
     const int L = s_len[bi], nt = n_tiles<C::kTile>(L, a.n_win), t0 = first_tile<C::kTile>(L, a.n_win);
@@ -519,29 +530,32 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
     const unsigned ue = min(u1, seg1);
     WarpState<T, D, G> w;
     w.start(a, bi, gi, s_q, lane, t);
-    for (unsigned v = u; v < ue; ++v) {
-      const unsigned n = v - u0;
-      if ((int)(n % C::kGroups) != group || failed) continue;
-      const int st = (int)(n % C::kStages);
-      if (!tc::mbar_wait(tc::smem_u32(&s_full[st]), (n / C::kStages) & 1, a.poll)) {
-        failed = true;  // the warps that share the barriers below go on meeting them
-        continue;
+    for (unsigned v = u0 + group + i * C::kGroups; v < ue; v += C::kGroups, ++i) {
+      const int st = (int)(i % C::kStages);
+      if (!failed && !(bad >> st & 1u)) {
+        // a warp that gives up goes on meeting the barriers below
+        if (__all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&s_full[group][st]), phases >> st & 1u, a.poll))) {
+          phases ^= 1u << st;
+          const int valid = min(C::kTile, L - (t0 + (int)(v - seg0)) * C::kTile);
+          const uint32_t sk = ring + st * C::kStage;
+          if (row0 < valid) w.consume(sk, sk + C::kHalf, row0, valid, scale, s_q, s_p, lane);
+        } else {
+          failed = true;
+          stuck = i;
+        }
       }
-      const int valid = s_bad[st] ? 0 : min(C::kTile, L - (t0 + (int)(v - seg0)) * C::kTile);
-      const uint32_t sk = ring + st * C::kStage;
-      if (row0 < valid)
-        w.consume(sk, sk + C::kHalf, row0, valid, scale, s_q, s_p + warp * 16 * G, lane);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tc::smem_u32(&s_empty[st]));
+      if (i + C::kStages < mine) {  // refill the stage once the group is done with it
+        group_sync();
+        if (!failed) issue();
+      }
     }
-    failed = __any_sync(0xffffffffu, failed);
     if (failed && lane == 0) {
       set_error(a.err, kErrTimeout);
       s_abort = 1;
     }
     // join the warps
     w.finish(s_join + warp * G * D, s_m[warp], s_l[warp], lane);
-    bar_consumers();
+    __syncthreads();
     const bool whole = u == seg0 && ue == seg1;
     const bool aborted = s_abort != 0;
     const int slot = 2 * blockIdx.x + (seg0 >= u0 ? 1 : 0);
@@ -566,74 +580,93 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
         __stcg(reinterpret_cast<float4*>(ka.part + (size_t)slot * G * D) + t, acc);
         // NaN as the maximum (which is never one) marks a part that was given up
         if (t * 4 % D == 0) __stcg(ka.part_ml + (size_t)slot * G + hh, make_float2(aborted ? NAN : M, z));
-        __threadfence();
       }
     }
-    bar_consumers();  // the warps' places are free again, and the partial is written
+    __syncthreads();  // the warps' places are free again, and the partial is written
     if (!whole) {
       const int first = (int)(seg0 / per), last = (int)((seg1 - 1) / per), n = last - first + 1;
       if (t == 0) {
+        __threadfence();  // the CTA's partial, ordered before by the barrier, is visible before the ticket
         // counts n - 1 up to itself and starts again at 0: ready for the next call
         s_last = atomicInc(ka.ticket + (size_t)bi * a.g + gi, (unsigned)(n - 1)) == (unsigned)(n - 1);
         __threadfence();
       }
-      bar_consumers();
+      __syncthreads();
       if (s_last) {
         // part j of the segment: slot 1 of the CTA where it begins, slot 0 of the others
         auto slot_of = [&](int j) { return (size_t)(2 * (first + j) + (j == 0 ? 1 : 0)); };
+        // kNp threads share a float4 column: each sums every kNp-th part, then they are joined.
+        // The first kFirst parts are on their way while the weights are computed.
+        constexpr int kNp = kDenseThreads / C::kVec, kFirst = 4;
+        const int v = t % C::kVec, np = t / C::kVec, hv = v * 4 / D;
+        auto part_at = [&](int j) { return __ldcg(reinterpret_cast<const float4*>(ka.part + slot_of(j) * G * D) + v); };
+        float4 x[kFirst];
+#pragma unroll
+        for (int i = 0; i < kFirst; ++i)
+          x[i] = np + i * kNp < n ? part_at(np + i * kNp) : make_float4(0.f, 0.f, 0.f, 0.f);
         bool gone = false;
-        for (int hh = warp; hh < G; hh += kDenseWarps) {
+        if (warp < G) {
+          constexpr int kMl = (kDenseCtas + 31) / 32;
+          float2 ml[kMl];
           float M = -INFINITY, z = 0.f;
-          for (int j = lane; j < n; j += 32) {
-            const float2 ml = __ldcg(ka.part_ml + slot_of(j) * G + hh);
-            gone |= ml.x != ml.x;
-            M = fmaxf(M, ml.x);
+#pragma unroll
+          for (int i = 0; i < kMl; ++i) {
+            ml[i] = lane + 32 * i < n ? __ldcg(ka.part_ml + slot_of(lane + 32 * i) * G + warp) : make_float2(-INFINITY, 0.f);
+            gone |= ml[i].x != ml[i].x;
+            M = fmaxf(M, ml[i].x);
           }
           M = warp_max(M);
           const float base = M == -INFINITY ? 0.f : M;
-          for (int j = lane; j < n; j += 32) {
-            const float2 ml = __ldcg(ka.part_ml + slot_of(j) * G + hh);
-            const float e = exp2f(ml.x - base);
-            s_join[hh * n + j] = e;
-            z = fmaf(e, ml.y, z);
+#pragma unroll
+          for (int i = 0; i < kMl; ++i) {
+            const float e = exp2f(ml[i].x - base);
+            if (lane + 32 * i < n) s_join[warp * n + lane + 32 * i] = e;
+            z = fmaf(e, ml[i].y, z);
           }
           z = warp_sum(z);
           if (lane == 0) {
-            s_M[hh] = M;
-            s_z[hh] = z;
+            s_M[warp] = M;
+            s_z[warp] = z;
           }
         }
         if (gone) s_abort = 1;
-        bar_consumers();
-        // kNp threads share a float4 column: each sums every kNp-th part, then they are joined
-        constexpr int kNp = kConsumers / C::kVec;
-        const int v = t % C::kVec, np = t / C::kVec, hh = v * 4 / D;
+        __syncthreads();
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](const float4& y, int j) {
+          const float e = s_join[hv * n + j];
+          acc.x = fmaf(e, y.x, acc.x); acc.y = fmaf(e, y.y, acc.y);
+          acc.z = fmaf(e, y.z, acc.z); acc.w = fmaf(e, y.w, acc.w);
+        };
+#pragma unroll
+        for (int i = 0; i < kFirst; ++i)
+          if (np + i * kNp < n) add(x[i], np + i * kNp);
 #pragma unroll 8
-        for (int j = np; j < n; j += kNp) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(ka.part + slot_of(j) * G * D) + v);
-          const float e = s_join[hh * n + j];
-          acc.x = fmaf(e, x.x, acc.x); acc.y = fmaf(e, x.y, acc.y);
-          acc.z = fmaf(e, x.z, acc.z); acc.w = fmaf(e, x.w, acc.w);
-        }
+        for (int j = np + kFirst * kNp; j < n; j += kNp) add(part_at(j), j);
         if constexpr (kNp > 1) {
           float4* sj = reinterpret_cast<float4*>(s_join + 1536);  // behind the weights: G n <= 1184
           sj[np * C::kVec + v] = acc;
-          bar_consumers();
+          __syncthreads();
           if (np == 0) {
 #pragma unroll
             for (int k = 1; k < kNp; ++k) {
-              const float4 x = sj[k * C::kVec + v];
-              acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+              const float4 y = sj[k * C::kVec + v];
+              acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
             }
           }
         }
-        if (np == 0 && !s_abort) write_row(bi, gi, v, acc, s_M[hh], s_z[hh]);
-        bar_consumers();
+        if (np == 0 && !s_abort) write_row(bi, gi, v, acc, s_M[hv], s_z[hv]);
+        __syncthreads();
       }
     }
     u = ue;
   }
+  // A feeding warp that gave up has copies in flight (units stuck .. issued - 1): they land before
+  // the CTA can end.
+  if (feeds && failed)
+    for (; stuck < issued; ++stuck) {
+      const int st = (int)(stuck % C::kStages);
+      if (!(bad >> st & 1u)) tc::mbar_wait(tc::smem_u32(&s_full[group][st]), phases >> st & 1u, kDrainPolls);
+    }
 }
 
 // ---- host -------------------------------------------------------------------
@@ -695,7 +728,7 @@ static cudaError_t launch_dense_g(const DenseKernelArgs& ka, cudaStream_t st) {
 
 // Units are counted in 32 bits, and the pool's blocks are a TMA coordinate.
 bool decode_dense_supported(int g, int max_chunks, int n_pages) {
-  return 2ll * g * max_chunks < (1ll << 31) && (long long)n_pages * g < (1ll << 31);
+  return (long long)kDenseMaxTiles * g * max_chunks < (1ll << 31) && (long long)n_pages * g < (1ll << 31);
 }
 DenseScratch decode_dense_scratch(int b, int h, int g, int d) {
   DenseScratch s;
@@ -711,7 +744,7 @@ cudaError_t run_decode_dense(const DenseArgs& a, void* scratch, cudaStream_t st)
   const DenseScratch S = decode_dense_scratch(a.b, a.h, a.g, a.d);
   const size_t es = a.bf16 ? 2 : 4;
   DenseKernelArgs ka;
-  const int rows = a.bf16 ? 64 : 32;
+  const int rows = a.bf16 ? DenseCfg<__nv_bfloat16, 64, 1>::kTile : DenseCfg<float, 64, 1>::kTile;
   if (!encode_pages_map(&ka.tmap_k, a.k_pages, a.d, (long long)a.n_pages * a.g, a.bf16, rows) ||
       !encode_pages_map(&ka.tmap_v, a.v_pages, a.d, (long long)a.n_pages * a.g, a.bf16, rows))
     return cudaErrorInvalidValue;
@@ -720,7 +753,7 @@ cudaError_t run_decode_dense(const DenseArgs& a, void* scratch, cudaStream_t st)
   ka.part_ml = reinterpret_cast<float2*>(w + S.part_ml);
   ka.ticket = reinterpret_cast<unsigned*>(w + S.ticket);
   // sequences of one launch: their prefix sums fit shared memory, their units 32 bits
-  const long long fit = ((1ll << 31) - 1) / (2ll * a.g * a.max_chunks);
+  const long long fit = ((1ll << 31) - 1) / ((long long)kDenseMaxTiles * a.g * a.max_chunks);
   const int step = (int)(fit < kDenseSeqs ? fit : kDenseSeqs);
   for (int b0 = 0; b0 < a.b; b0 += step) {
     ka.a = a;
