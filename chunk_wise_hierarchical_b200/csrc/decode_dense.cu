@@ -8,23 +8,24 @@
 // beyond the CUDA cores -- so the bf16 products run on the tensor cores with the keys as the
 // M = 16 rows and the heads as the N = 8 columns of mma.m16n8k16.
 //
-// Split.  The tiles (kTile keys of one (sequence, KV head), "units") of the whole batch are
-// numbered in a row, and CTA i of kDenseCtas takes units [i per, (i + 1) per): every SM reads
-// the same number of bytes whatever the lengths are, and the host needs none of them (the
-// launch is the same for every step, so a graph can hold it).  A (sequence, KV head) whose
-// units all lie in one CTA is written by it.  One that is cut leaves partials (max, sum,
-// unnormalised output) in the workspace, at most two per CTA; the CTA that takes the last
-// ticket joins them in CTA order, so that the result does not depend on who that is.  No CTA
-// waits for another.
+// Split.  The tiles (kTile keys of one (sequence, KV head), "units", 16 KB of K and V each) of
+// the whole batch are numbered in a row.  CTA i of kDenseCtas takes units [i per, (i + 1) per),
+// and each of its warps an equal run of those: every SM reads the same number of bytes whatever
+// the lengths are, and the host needs none of them (the launch is the same for every step, so a
+// graph can hold it).  A warp writes the (sequence, KV head)s that lie in its run; of those that
+// are cut -- at most two of a warp -- it leaves partials (max, sum, unnormalised output) in
+// shared memory, which the CTA joins when its warps are done.  A (sequence, KV head) that is cut
+// between CTAs -- at most two of a CTA -- leaves a partial in the workspace, and the CTA that
+// takes the last ticket joins them (in two steps where there are many).  Partials are joined in
+// the order of the keys, so that the result does not depend on who comes last.  Nobody waits
+// for another CTA.
 //
-// Within a CTA, the kTileWarps warps of group j take units j, j + kGroups, ... and feed
-// themselves: they read their part of the block table 32 units at a time, and a lane of the
-// group's first warp refills a stage of the group's own ring by TMA (K and V tile, 128-byte
-// swizzle) as soon as the group has consumed it.  Nobody else is waited for: each warp keeps its
-// own running maximum, sum and output, and the warps are joined in shared memory at the end of
-// each (sequence, KV head).  (One producer warp feeding all through full and empty barriers was
-// tried first: its loop took about 500 cycles a unit, which 16 KB units -- 700 cycles of the SM's
-// share of HBM -- do not hide.)
+// A warp feeds itself: it reads its part of the block table 32 units at a time, and its lane 0
+// refills the stages of the warp's ring by TMA (128-byte swizzle) as soon as the warp has
+// consumed them.  What was tried before: one producer warp and full and empty barriers (its loop
+// took about 500 cycles a unit; a 16 KB unit is 700 cycles of the SM's share of HBM), and units
+// dealt to the warps in turn, joined at the end of every (sequence, KV head) (about 2 us each,
+// which batches of short sequences do not hide).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -43,31 +44,37 @@ constexpr int kDenseWarps = 8;
 constexpr int kDenseThreads = kDenseWarps * 32;
 constexpr int kDenseCtas = 148;          // one per SM
 constexpr int kDenseSeqs = 1024;         // sequences of one launch (their prefix sums in shared memory)
-constexpr int kDenseRing = 128 * 1024;   // bytes of the rings of a CTA
-constexpr int kDenseMaxTiles = 2;        // units of a chunk and KV head, at most
-constexpr int kDenseMinUnits = 2;        // units of a CTA, at least
+constexpr int kDenseMaxTiles = 4;        // units of a chunk and KV head, at most
+constexpr int kDenseMinUnits = 4;        // units of a CTA, at least
+constexpr int kJoinMost = 32;            // partials joined in one step (one per lane)
+constexpr int kJoinBlock = 13;           // more are joined in blocks of this many first
+
+// Bytes of a warp's ring.  Eight warps have 128 KB in flight, which reaches the card's read
+// rate; 192 KB lose some of it again (one 512K context, 7B heads: 306 us with 128 KB, 317 us
+// with 192 KB), and so do smaller units.
+constexpr int kDenseRing = 16 * 1024;
 
 // T element, D head dim, G heads per KV head.
 template <typename T, int D, int G>
 struct DenseCfg {
-  static constexpr int kTile = sizeof(T) == 2 ? 64 : 32;         // keys per unit
-  static constexpr int kTileWarps = 2;                           // warps that share a unit
-  static constexpr int kSlice = kTile / kTileWarps;              // keys of it that one warp takes
-  static constexpr int kGroups = kDenseWarps / kTileWarps;
+  static constexpr int kTile = 8192 / (D * (int)sizeof(T));      // keys per unit: 64, 32 (bf16), 32, 16 (fp32)
   static constexpr int kCols = 128 / (int)sizeof(T);             // columns of a swizzled sub-tile
   static constexpr int kSubs = D / kCols;
   static constexpr uint32_t kSub = kTile * 128u;                 // bytes of a sub-tile
   static constexpr uint32_t kHalf = kSubs * kSub;                // K (or V) of a stage
   static constexpr uint32_t kStage = 2 * kHalf;
-  static constexpr int kStages = kDenseRing / kGroups / (int)kStage;  // of a group
+  static constexpr int kStages = kDenseRing / (int)kStage;
   static constexpr int kVec = G * D / 4;                         // float4 columns of an output
+  static constexpr uint32_t kRings = kDenseWarps * kDenseRing;
   // shared memory behind the rings, in floats
-  static constexpr int kJoin = kDenseWarps * G * D > 2560 ? kDenseWarps * G * D : 2560;
-  static constexpr int kQ = sizeof(T) == 4 ? G * D : 0;
-  static constexpr int kP = sizeof(T) == 4 ? kDenseWarps * 16 * G : 0;
-  static constexpr uint32_t kRings = kGroups * kStages * kStage;
-  static constexpr size_t kSmem = 1024 + (size_t)kRings + 4ull * (kJoin + kQ + kP);
-  static_assert(kStages >= 1 && kSmem <= 227 * 1024 - 10 * 1024, "room for the static shared variables");
+  static constexpr int kHeads = kDenseWarps * G * D;             // the warps' first partials (see slot_of)
+  static constexpr int kWeights = G * kJoinMost;
+  static constexpr int kSums = kDenseThreads * 4;
+  static constexpr int kQ = sizeof(T) == 4 ? G * D : 0;          // per warp: queries and weights of the fp32 path
+  static constexpr int kP = sizeof(T) == 4 ? 16 * G : 0;
+  static constexpr size_t kSmem = 1024 + (size_t)kRings + 4ull * (kHeads + kWeights + kSums + kDenseWarps * (kQ + kP));
+  static_assert(kStages >= 1 && kTile % 16 == 0 && G * D * 4 <= kDenseRing, "a unit fills a stage, an output fits one");
+  static_assert(kSmem <= 227 * 1024 - 10 * 1024, "room for the static shared variables");
 };
 
 struct alignas(64) DenseKernelArgs {
@@ -75,6 +82,7 @@ struct alignas(64) DenseKernelArgs {
   DenseArgs a;                 // of this launch's sequences
   float* part;                 // [2 kDenseCtas][G D]
   float2* part_ml;             // [2 kDenseCtas][G]
+  unsigned* block_ticket;      // [2 kDenseCtas], zero between calls
   unsigned* ticket;            // [b g], zero between calls
 };
 
@@ -119,16 +127,23 @@ __device__ __forceinline__ float raise_max(float& m, float t, float& base) {
   return c;
 }
 
-// bf16: the warp's state over its slices of 16 NS keys.  Lane l holds heads 2 (l % 4), + 1, as the
-// columns of the transposed score tile S^T = K Q^T and of O^T = V^T P^T.  P is split into
+// 1 / z, and log sum exp from the maximum (in units of log 2) and the sum; a row that no finite
+// logit reached has z = 0 and becomes zero, -inf.
+__device__ __forceinline__ float inverse_sum(float z) { return z == 0.f ? 0.f : 1.f / z; }
+__device__ __forceinline__ float log_sum(float m, float z) {
+  return z == 0.f ? -INFINITY : (m + log2f(z)) * 0.69314718055994531f;
+}
+
+// bf16: the warp's state.  Lane l holds heads 2 (l % 4), + 1, as the columns of the transposed score tile S^T = K Q^T and of O^T = V^T P^T.  P is split into
 // bf16 hi + lo parts (two products), so that its rounding (2^-17) stays below that of the
 // output; the tensor cores have the room at this byte rate.
-template <int D, int G, int NS>
+template <int D, int G>
 struct WarpStateBf16 {
+  static constexpr int NS = DenseCfg<__nv_bfloat16, D, G>::kTile / 16;  // 16-key products of a unit
   float m[2], l[2], o[D / 16][4];
   uint32_t q[D / 16][2];
 
-  __device__ void start(const DenseArgs& a, int bi, int gi, float*, int lane, int) {
+  __device__ void start(const DenseArgs& a, int bi, int gi, float*, int lane) {
     const int hh = lane >> 2;
     const uint32_t* row = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) +
                                                             ((size_t)bi * a.h + gi * G + hh) * D);
@@ -142,9 +157,9 @@ struct WarpStateBf16 {
     l[0] = l[1] = 0.f;
   }
 
-  // Keys [row0, row0 + 16 NS) of a tile with `valid` keys (> row0): NS 16-key products side by
-  // side, one step of the running maximum for all.
-  __device__ void consume(uint32_t sk, uint32_t sv, int row0, int valid, float scale, const float*, float*, int lane) {
+  // A unit with `valid` keys (> 0): NS 16-key products side by side, one step of the running
+  // maximum for all.
+  __device__ void consume(uint32_t sk, uint32_t sv, int valid, float scale, const float*, float*, int lane) {
     constexpr uint32_t kSub = DenseCfg<__nv_bfloat16, D, G>::kSub;
     float s[NS][4];
 #pragma unroll
@@ -154,17 +169,17 @@ struct WarpStateBf16 {
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         uint32_t f[4];
-        ldsm4(sk + (k >> 2) * kSub + tc::sw128_chunk(row0 + 16 * i + (lane & 15), (k & 3) * 2 + (lane >> 4)), f);
+        ldsm4(sk + (k >> 2) * kSub + tc::sw128_chunk(16 * i + (lane & 15), (k & 3) * 2 + (lane >> 4)), f);
         mma16816(s[i], f, q[k][0], q[k][1]);
       }
     }
-    // s[i]: keys r, r (heads 2c, 2c + 1), r + 8, r + 8, r = row0 + 16 i + lane / 4
+    // s[i]: keys r, r (heads 2c, 2c + 1), r + 8, r + 8, r = 16 i + lane / 4
     float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NS; ++i)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const bool ok = row0 + 16 * i + 8 * e + (lane >> 2) < valid;
+        const bool ok = 16 * i + 8 * e + (lane >> 2) < valid;
         s[i][2 * e] = ok ? s[i][2 * e] * scale : -INFINITY;
         s[i][2 * e + 1] = ok ? s[i][2 * e + 1] * scale : -INFINITY;
         t0 = fmaxf(t0, s[i][2 * e]);
@@ -198,11 +213,11 @@ struct WarpStateBf16 {
         ph[i][e] = transpose8(h);
         pl[i][e] = transpose8(tc::pack_bf16x2(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u)));
         // values behind the last key may be anything: they are cleared, not only weighted by 0
-        const int k0 = row0 + 16 * i + 8 * e + (lane & 3) * 2;
+        const int k0 = 16 * i + 8 * e + (lane & 3) * 2;
         keep[i][e] = (k0 < valid ? 0xffffu : 0u) | (k0 + 1 < valid ? 0xffff0000u : 0u);
       }
-    const bool tail = row0 + 16 * NS > valid;
-    const uint32_t vrow = row0 + (lane & 7) + ((lane >> 4) << 3), vch = (lane >> 3) & 1;
+    const bool tail = 16 * NS > valid;
+    const uint32_t vrow = (lane & 7) + ((lane >> 4) << 3), vch = (lane >> 3) & 1;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
 #pragma unroll
@@ -218,21 +233,37 @@ struct WarpStateBf16 {
     }
   }
 
-  // so [G][D], sm and sl [G]: this warp's place in shared memory
-  __device__ void finish(float* so, float* sm, float* sl, int lane) {
+  // The sums over all of the warp's keys (the lanes hold shares of l until here).
+  __device__ void finish() {
 #pragma unroll
     for (int d = 4; d < 32; d <<= 1) {
       l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
       l[1] += __shfl_xor_sync(0xffffffffu, l[1], d);
     }
+  }
+  // The result: rows out [G][D], lse [G] (or nullptr).
+  __device__ void write(__nv_bfloat16* out, float* lse, int lane) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int hh = (lane & 3) * 2 + e;
       if (hh < G) {
-        if (lane < 4) {
-          sm[hh] = m[e];
-          sl[hh] = l[e];
+        const float inv = inverse_sum(l[e]);
+        if (lse && lane < 4) lse[hh] = log_sum(m[e], l[e]);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          out[hh * D + k * 16 + (lane >> 2)] = __float2bfloat16_rn(o[k][e] * inv);
+          out[hh * D + k * 16 + 8 + (lane >> 2)] = __float2bfloat16_rn(o[k][2 + e] * inv);
         }
+      }
+    }
+  }
+  // The partial: so [G][D], ml [G].
+  __device__ void leave(float* so, float2* ml, int lane) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int hh = (lane & 3) * 2 + e;
+      if (hh < G) {
+        if (lane < 4) ml[hh] = make_float2(m[e], l[e]);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           so[hh * D + k * 16 + (lane >> 2)] = o[k][e];
@@ -251,10 +282,10 @@ struct WarpStateF32 {
   static constexpr int kCpl = D / 32;
   float m[G], l[G], o[G][kCpl];
 
-  __device__ void start(const DenseArgs& a, int bi, int gi, float* sq, int, int ct) {
+  __device__ void start(const DenseArgs& a, int bi, int gi, float* sq, int lane) {
     const float* row = static_cast<const float*>(a.q) + ((size_t)bi * a.h + gi * G) * D;
-    for (int x = ct; x < G * D; x += kDenseThreads) sq[x] = __ldg(row + x);
-    __syncthreads();
+    for (int x = lane; x < G * D; x += 32) sq[x] = __ldg(row + x);
+    __syncwarp();
 #pragma unroll
     for (int hh = 0; hh < G; ++hh) {
       m[hh] = -INFINITY;
@@ -264,9 +295,12 @@ struct WarpStateF32 {
     }
   }
 
-  // Keys [row0, row0 + 16) of a tile with `valid` keys (> row0).
-  __device__ void consume(uint32_t sk, uint32_t sv, int row0, int valid, float scale, const float* sq, float* sp,
-                          int lane) {
+  // A unit with `valid` keys (> 0), 16 at a time.
+  __device__ void consume(uint32_t sk, uint32_t sv, int valid, float scale, const float* sq, float* sp, int lane) {
+    for (int row0 = 0; row0 < valid; row0 += 16) slice(sk, sv, row0, valid, scale, sq, sp, lane);
+  }
+  __device__ __forceinline__ void slice(uint32_t sk, uint32_t sv, int row0, int valid, float scale, const float* sq,
+                                        float* sp, int lane) {
     constexpr uint32_t kSub = DenseCfg<float, D, G>::kSub;
     const int rr = lane >> 2, c = lane & 3;
     const int pr = ((rr & 1) << 2) | (rr >> 1);
@@ -331,15 +365,25 @@ struct WarpStateF32 {
     __syncwarp();
   }
 
-  __device__ void finish(float* so, float* sm, float* sl, int lane) {
+  __device__ void finish() {
 #pragma unroll
-    for (int hh = 0; hh < G; ++hh) {
+    for (int hh = 0; hh < G; ++hh)
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], d);
-      if (lane == 0) {
-        sm[hh] = m[hh];
-        sl[hh] = l[hh];
-      }
+  }
+  __device__ void write(float* out, float* lse, int lane) {
+#pragma unroll
+    for (int hh = 0; hh < G; ++hh) {
+      const float inv = inverse_sum(l[hh]);
+      if (lse && lane == 0) lse[hh] = log_sum(m[hh], l[hh]);
+#pragma unroll
+      for (int x = 0; x < kCpl; ++x) out[hh * D + lane * kCpl + x] = o[hh][x] * inv;
+    }
+  }
+  __device__ void leave(float* so, float2* ml, int lane) {
+#pragma unroll
+    for (int hh = 0; hh < G; ++hh) {
+      if (lane == 0) ml[hh] = make_float2(m[hh], l[hh]);
 #pragma unroll
       for (int x = 0; x < kCpl; ++x) so[hh * D + lane * kCpl + x] = o[hh][x];
     }
@@ -347,8 +391,7 @@ struct WarpStateF32 {
 };
 
 template <typename T, int D, int G> struct WarpState;
-template <int D, int G>
-struct WarpState<__nv_bfloat16, D, G> : WarpStateBf16<D, G, DenseCfg<__nv_bfloat16, D, G>::kSlice / 16> {};
+template <int D, int G> struct WarpState<__nv_bfloat16, D, G> : WarpStateBf16<D, G> {};
 template <int D, int G> struct WarpState<float, D, G> : WarpStateF32<D, G> {};
 
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
@@ -380,6 +423,12 @@ __device__ __forceinline__ int seq_of(const unsigned* prefix, int n, unsigned u)
 
 }  // namespace
 
+// Segment of units: one (sequence, KV head).
+struct Segment {
+  int bi, gi, nt;      // nt: its units
+  unsigned lo, hi;     // [lo, hi)
+};
+
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __grid_constant__ DenseKernelArgs ka) {
   using C = DenseCfg<T, D, G>;
@@ -387,23 +436,31 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
   __shared__ unsigned s_prefix[kDenseSeqs + 1];  // units before each sequence
   __shared__ int s_len[kDenseSeqs];
   __shared__ __align__(16) unsigned s_scan[kDenseWarps];
-  __shared__ uint64_t s_full[C::kGroups][C::kStages];
-  __shared__ float s_m[kDenseWarps][G], s_l[kDenseWarps][G], s_M[G], s_z[G];
-  __shared__ int s_abort, s_last;
+  __shared__ uint64_t s_full[kDenseWarps][C::kStages];
+  __shared__ Segment s_seg[2 * kDenseWarps];     // the segment in each warp slot (nt 0: none)
+  __shared__ Segment s_cut[2];                   // the segments of u0 and u1 - 1, where they are cut (nt 0: not)
+  __shared__ float2 s_ml[2 * kDenseWarps][G];
+  __shared__ float s_M[G], s_z[G];
+  __shared__ int s_abort, s_last[2];
 
   const DenseArgs& a = ka.a;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const uint32_t ring0 = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
-  const int group = warp / C::kTileWarps, row0 = warp % C::kTileWarps * C::kSlice;
-  const bool feeds = warp % C::kTileWarps == 0;  // the group's first warp issues its copies
-  const uint32_t ring = ring0 + group * C::kStages * C::kStage;
-  float* s_join = reinterpret_cast<float*>(smem_raw + (ring0 - tc::smem_u32(smem_raw)) + C::kRings);
-  float* s_q = s_join + C::kJoin;
-  float* s_p = s_q + C::kQ + warp * 16 * G;
+  const uint32_t ring = ring0 + warp * kDenseRing;
+  float* s_ring = reinterpret_cast<float*>(smem_raw + (ring0 - tc::smem_u32(smem_raw)));
+  float* s_heads = s_ring + C::kRings / 4;
+  float* s_weights = s_heads + C::kHeads;
+  float* s_sums = s_weights + C::kWeights;
+  float* s_q = s_sums + C::kSums + warp * (C::kQ + C::kP);
+  float* s_p = s_q + C::kQ;
+  // A warp's slots: 2 w for the segment that began before its run, 2 w + 1 for the one that goes
+  // on behind it.  The second is left when the warp's ring is no longer in use, and lies there.
+  auto slot_of = [&](int x) { return x & 1 ? s_ring + (x >> 1) * (kDenseRing / 4) : s_heads + (x >> 1) * G * D; };
 
-  if (feeds && lane == 0) {
-    for (int s = 0; s < C::kStages; ++s) tc::mbar_init(tc::smem_u32(&s_full[group][s]), 1);
+  if (lane == 0) {
+    for (int s = 0; s < C::kStages; ++s) tc::mbar_init(tc::smem_u32(&s_full[warp][s]), 1);
     tc::mbar_fence_init();
+    s_seg[2 * warp].nt = s_seg[2 * warp + 1].nt = 0;
   }
   if (t == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&ka.tmap_k) : "memory");
@@ -445,30 +502,40 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
   const unsigned total = s_prefix[a.b];
   const unsigned per = max((unsigned)kDenseMinUnits, (total + kDenseCtas - 1) / kDenseCtas);
   const unsigned u0 = min(total, blockIdx.x * per), u1 = min(total, u0 + per);
+  const unsigned per_warp = (u1 - u0 + kDenseWarps - 1) / kDenseWarps;
+  const unsigned w0 = min(u1, u0 + warp * per_warp), w1 = min(u1, w0 + per_warp);
+  auto segment_of = [&](int b, unsigned u) {  // the segment of unit u of sequence b
+    Segment g;
+    g.bi = b;
+    g.nt = n_tiles<C::kTile>(s_len[b], a.n_win);
+    g.gi = (int)(u - s_prefix[b]) / g.nt;
+    g.lo = s_prefix[b] + (unsigned)g.gi * g.nt;
+    g.hi = g.lo + g.nt;
+    return g;
+  };
 
-  // The group's units: number i is unit u0 + group + kGroups i.  Lane j knows the place of number
-  // base + j (z: block of the pool, -1 for a bad page; y: row in it) and of the 32 after those.
+  T* out = static_cast<T*>(a.out);
+  // ---- the warp's run: units w0 + 0, 1, ...; lane j knows the place of number base + j (z: block
+  // of the pool, -1 for a bad page; y: row in it) and of the 32 after those
   auto locate = [&](unsigned i, int& y, int& z) {
-    const unsigned u = u0 + group + i * C::kGroups;
+    const unsigned u = w0 + i;
     z = -1;
     y = 0;
-    if (u >= u1) return;
+    if (u >= w1) return;
     const int b = seq_of(s_prefix, a.b, u);
-    const int L = s_len[b];
-    const int nt = n_tiles<C::kTile>(L, a.n_win);
-    const int rem = (int)(u - s_prefix[b]);
-    const int tile = first_tile<C::kTile>(L, a.n_win) + rem % nt;
+    const Segment g = segment_of(b, u);
+    const int tile = first_tile<C::kTile>(s_len[b], a.n_win) + (int)(u - g.lo);
     const int page = a.block_table[(size_t)b * a.max_chunks + tile * C::kTile / kChunk];
     y = tile * C::kTile % kChunk;
-    if (page >= 0 && page < a.n_pages) z = page * a.g + rem / nt;
+    if (page >= 0 && page < a.n_pages) z = page * a.g + g.gi;
     else set_error(a.err, kErrBadPage);
   };
-  const unsigned mine = u0 + group < u1 ? (u1 - u0 - group + C::kGroups - 1) / C::kGroups : 0;
+  const unsigned mine = w1 - w0;
   unsigned issued = 0, base = 0, bad = 0;  // bad: bit s, stage s has no page
   int y, z, yn = 0, zn = -1;
   locate(lane, y, z);
   if (mine > 32) locate(32 + lane, yn, zn);
-  auto issue = [&]() {  // the next unit's copies (every lane of the group calls it)
+  auto issue = [&]() {  // the next unit's copies (all lanes call it)
     if (issued - base == 32) {
       base += 32;
       y = yn;
@@ -478,8 +545,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
     const int yi = __shfl_sync(0xffffffffu, y, issued - base), zi = __shfl_sync(0xffffffffu, z, issued - base);
     const int st = (int)(issued % C::kStages);
     bad = zi < 0 ? bad | 1u << st : bad & ~(1u << st);
-    if (feeds && lane == 0 && zi >= 0) {
-      const uint32_t full = tc::smem_u32(&s_full[group][st]), dst = ring + st * C::kStage;
+    if (lane == 0 && zi >= 0) {
+      const uint32_t full = tc::smem_u32(&s_full[warp][st]), dst = ring + st * C::kStage;
       tc::fence_async_smem();  // the stage's last reads, before the copies into it
       tc::mbar_arrive_expect_tx(full, C::kStage);
 #pragma unroll
@@ -493,12 +560,18 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
   while (issued < mine && issued < (unsigned)C::kStages) issue();
   unsigned phases = 0;  // bit s: parity of the next fill of stage s to wait for
 
-  auto group_sync = [&]() {
-    if constexpr (C::kTileWarps == 1) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(C::kTileWarps * 32) : "memory");
-  };
+  if (t == 0) {  // for the end, while the first units are on their way
+    s_cut[0].nt = s_cut[1].nt = 0;
+    if (u0 < u1) {
+      const Segment first = segment_of(seq_of(s_prefix, a.b, u0), u0);
+      if (first.lo < u0 || first.hi > u1) s_cut[0] = first;
+      if (first.hi < u1) {
+        const Segment last = segment_of(seq_of(s_prefix, a.b, u1 - 1), u1 - 1);
+        if (last.hi > u1) s_cut[1] = last;
+      }
+    }
+  }
 
-  T* out = static_cast<T*>(a.out);
   // sequences without keys
   for (int b = blockIdx.x; b < a.b; b += kDenseCtas) {
     if (s_len[b] > 0) continue;
@@ -507,166 +580,210 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
     if (a.lse)
       for (int x = t; x < a.h; x += kDenseThreads) a.lse[(size_t)b * a.h + x] = -INFINITY;
   }
+
   const float scale = a.scale * 1.4426950408889634f;  // logits in units of log 2
   bool failed = false;
-
-  // Writes head hh's columns [col, col + 4) and, once per head, its log-sum-exp.
-  auto write_row = [&](int bi, int gi, int x, float4 acc, float M, float z) {
-    const int hh = x * 4 / D;
-    const size_t row = (size_t)bi * a.h + gi * G + hh;
-    const float inv = z == 0.f ? 0.f : 1.f / z;  // no key with a finite logit: a zero row
-    acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
-    store4(out + row * D + x * 4 % D, acc);
-    if (a.lse && x * 4 % D == 0) a.lse[row] = z == 0.f ? -INFINITY : (M + log2f(z)) * 0.69314718055994531f;
-  };
-
-  int bi = u0 < u1 ? seq_of(s_prefix, a.b, u0) : 0;
-  unsigned i = 0, stuck = 0;  // the group's next unit; the one this warp gave up at
-  for (unsigned u = u0; u < u1;) {
+  int bi = w0 < w1 ? seq_of(s_prefix, a.b, w0) : 0;
+  unsigned u = w0;
+  while (u < w1) {
     while (s_prefix[bi + 1] <= u) ++bi;
-    const int L = s_len[bi], nt = n_tiles<C::kTile>(L, a.n_win), t0 = first_tile<C::kTile>(L, a.n_win);
-    const int gi = (int)(u - s_prefix[bi]) / nt;
-    const unsigned seg0 = s_prefix[bi] + (unsigned)gi * nt, seg1 = seg0 + nt;
-    const unsigned ue = min(u1, seg1);
+    const Segment g = segment_of(bi, u);
+    const unsigned ue = min(w1, g.hi);
+    const int first = first_tile<C::kTile>(s_len[bi], a.n_win);
     WarpState<T, D, G> w;
-    w.start(a, bi, gi, s_q, lane, t);
-    for (unsigned v = u0 + group + i * C::kGroups; v < ue; v += C::kGroups, ++i) {
+    w.start(a, bi, g.gi, s_q, lane);
+    for (; u < ue; ++u) {
+      const unsigned i = u - w0;
       const int st = (int)(i % C::kStages);
-      if (!failed && !(bad >> st & 1u)) {
-        // a warp that gives up goes on meeting the barriers below
-        if (__all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&s_full[group][st]), phases >> st & 1u, a.poll))) {
-          phases ^= 1u << st;
-          const int valid = min(C::kTile, L - (t0 + (int)(v - seg0)) * C::kTile);
-          const uint32_t sk = ring + st * C::kStage;
-          if (row0 < valid) w.consume(sk, sk + C::kHalf, row0, valid, scale, s_q, s_p, lane);
-        } else {
-          failed = true;
-          stuck = i;
-        }
+      if (!(bad >> st & 1u)) {
+        failed = !__all_sync(0xffffffffu, tc::mbar_wait(tc::smem_u32(&s_full[warp][st]), phases >> st & 1u, a.poll));
+        if (failed) break;
+        phases ^= 1u << st;
+        const uint32_t sk = ring + st * C::kStage;
+        w.consume(sk, sk + C::kHalf, min(C::kTile, s_len[bi] - (first + (int)(u - g.lo)) * C::kTile), scale, s_q, s_p,
+                  lane);
+        __syncwarp();
       }
-      if (i + C::kStages < mine) {  // refill the stage once the group is done with it
-        group_sync();
-        if (!failed) issue();
-      }
+      if (issued < mine) issue();
     }
-    if (failed && lane == 0) {
+    if (failed) break;
+    w.finish();
+    if (g.lo >= w0 && g.hi <= w1) {
+      const size_t row = (size_t)bi * a.h + g.gi * G;
+      w.write(out + row * D, a.lse ? a.lse + row : nullptr, lane);
+    } else {
+      const int x = 2 * warp + (g.lo >= w0 ? 1 : 0);
+      w.leave(slot_of(x), s_ml[x], lane);
+      if (lane == 0) s_seg[x] = g;
+    }
+  }
+  if (failed) {
+    // the copies in flight (units u .. w0 + issued - 1) land before the CTA can end
+    for (unsigned i = u - w0; i < issued; ++i) {
+      const int st = (int)(i % C::kStages);
+      if (!(bad >> st & 1u)) tc::mbar_wait(tc::smem_u32(&s_full[warp][st]), phases >> st & 1u, kDrainPolls);
+    }
+    if (lane == 0) {
       set_error(a.err, kErrTimeout);
       s_abort = 1;
     }
-    // join the warps
-    w.finish(s_join + warp * G * D, s_m[warp], s_l[warp], lane);
+  }
+  __syncthreads();
+  if (u0 == u1) return;
+  const bool aborted = s_abort != 0;
+
+  // ---- the cut segments of the CTA: a chain of slots begins with slot 0 or an odd one and goes
+  // on with the even slots of the warps behind it
+  auto write_row = [&](int b, int gi, int x, float4 acc, float M, float z) {  // float4 column x of [G][D]
+    const size_t row = (size_t)b * a.h + gi * G + x * 4 / D;
+    const float inv = inverse_sum(z);
+    acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
+    store4(out + row * D + x * 4 % D, acc);
+    if (a.lse && x * 4 % D == 0) a.lse[row] = log_sum(M, z);
+  };
+  // kNp threads share a float4 column: they take every kNp-th chain, or part
+  constexpr int kNp = kDenseThreads / C::kVec;
+  const int v = t % C::kVec, np = t / C::kVec, hv = v * 4 / D;
+  auto first_slot = [](int c) { return c == 0 ? 0 : 2 * c - 1; };
+  unsigned chains = __ballot_sync(0xffffffffu, lane <= kDenseWarps && s_seg[first_slot(min(lane, kDenseWarps))].nt != 0);
+  for (int k = 0; chains; chains &= chains - 1, ++k) {
+    if (k % kNp != np) continue;
+    const int x0 = first_slot(__ffs(chains) - 1), w_next = x0 / 2 + 1;
+    const Segment g = s_seg[x0];
+    int n = 1;  // slots of the chain: x0, then slots 2 w of the warps behind
+    while (w_next + n - 1 < kDenseWarps && s_seg[2 * (w_next + n - 1)].nt != 0 && s_seg[2 * (w_next + n - 1)].lo == g.lo) ++n;
+    auto member = [&](int i) { return i == 0 ? x0 : 2 * (w_next + i - 1); };
+    float M = -INFINITY, sum = 0.f;
+    for (int i = 0; i < n; ++i) M = fmaxf(M, s_ml[member(i)][hv].x);
+    const float top = M == -INFINITY ? 0.f : M;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < n; ++i) {
+      const float2 ml = s_ml[member(i)][hv];
+      const float e = exp2f(ml.x - top);
+      const float4 p = reinterpret_cast<const float4*>(slot_of(member(i)))[v];
+      sum = fmaf(e, ml.y, sum);
+      acc.x = fmaf(e, p.x, acc.x); acc.y = fmaf(e, p.y, acc.y);
+      acc.z = fmaf(e, p.z, acc.z); acc.w = fmaf(e, p.w, acc.w);
+    }
+    if (g.lo >= u0 && g.hi <= u1) {
+      if (!aborted) write_row(g.bi, g.gi, v, acc, M, sum);
+    } else {
+      const int slot = 2 * blockIdx.x + (g.lo >= u0 ? 1 : 0);
+      __stcg(reinterpret_cast<float4*>(ka.part + (size_t)slot * G * D) + v, acc);
+      if (v * 4 % D == 0) __stcg(ka.part_ml + (size_t)slot * G + hv, make_float2(M, sum));
+    }
+  }
+  if (aborted) {  // NaN as a maximum (which is never one) marks the parts that were given up
     __syncthreads();
-    const bool whole = u == seg0 && ue == seg1;
-    const bool aborted = s_abort != 0;
-    const int slot = 2 * blockIdx.x + (seg0 >= u0 ? 1 : 0);
-    if (t < C::kVec) {
-      const int hh = t * 4 / D;
-      float M = -INFINITY, z = 0.f;
+    if (t < 2 * G) __stcg(ka.part_ml + (size_t)(2 * blockIdx.x + t / G) * G + t % G, make_float2(NAN, 0.f));
+  }
+  __syncthreads();
+
+  // ---- segments cut between CTAs: the one of u0, and the one of u1 - 1
+  // Joins parts j0, j0 + step, ... (n <= kJoinMost) of the segment that begins in CTA `first`:
+  // the sum of the float4 column in the threads t < kVec, the rest in s_M and s_z.  Slot 1 of a CTA
+  // holds the part of a segment that begins there, slot 0 that of one that began before.
+  auto join = [&](int first, int j0, int step, int n) {
+    auto slot = [&](int j) { return (size_t)(2 * (first + j0 + j * step) + (j0 + j * step == 0 ? 1 : 0)); };
+    auto part_at = [&](int j) { return __ldcg(reinterpret_cast<const float4*>(ka.part + slot(j) * G * D) + v); };
+    constexpr int kFirst = 4;  // parts on their way while the weights are computed
+    float4 x[kFirst];
 #pragma unroll
-      for (int k = 0; k < kDenseWarps; ++k) M = fmaxf(M, s_m[k][hh]);
-      const float base = M == -INFINITY ? 0.f : M;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < kDenseWarps; ++k) {
-        const float e = exp2f(s_m[k][hh] - base);
-        const float4 x = *reinterpret_cast<const float4*>(s_join + k * G * D + t * 4);
-        z = fmaf(e, s_l[k][hh], z);
-        acc.x = fmaf(e, x.x, acc.x); acc.y = fmaf(e, x.y, acc.y);
-        acc.z = fmaf(e, x.z, acc.z); acc.w = fmaf(e, x.w, acc.w);
-      }
-      if (whole) {
-        if (!aborted) write_row(bi, gi, t, acc, M, z);
-      } else {
-        __stcg(reinterpret_cast<float4*>(ka.part + (size_t)slot * G * D) + t, acc);
-        // NaN as the maximum (which is never one) marks a part that was given up
-        if (t * 4 % D == 0) __stcg(ka.part_ml + (size_t)slot * G + hh, make_float2(aborted ? NAN : M, z));
+    for (int i = 0; i < kFirst; ++i)
+      x[i] = np + i * kNp < n ? part_at(np + i * kNp) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (warp < G) {
+      const float2 ml = lane < n ? __ldcg(ka.part_ml + slot(lane) * G + warp) : make_float2(-INFINITY, 0.f);
+      if (ml.x != ml.x) s_abort = 1;
+      const float M = warp_max(ml.x), e = exp2f(ml.x - (M == -INFINITY ? 0.f : M));
+      const float sum = warp_sum(e * ml.y);
+      s_weights[warp * kJoinMost + lane] = e;
+      if (lane == 0) {
+        s_M[warp] = M;
+        s_z[warp] = sum;
       }
     }
-    __syncthreads();  // the warps' places are free again, and the partial is written
-    if (!whole) {
-      const int first = (int)(seg0 / per), last = (int)((seg1 - 1) / per), n = last - first + 1;
-      if (t == 0) {
-        __threadfence();  // the CTA's partial, ordered before by the barrier, is visible before the ticket
-        // counts n - 1 up to itself and starts again at 0: ready for the next call
-        s_last = atomicInc(ka.ticket + (size_t)bi * a.g + gi, (unsigned)(n - 1)) == (unsigned)(n - 1);
-        __threadfence();
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4& p, int j) {
+      const float e = s_weights[hv * kJoinMost + j];
+      acc.x = fmaf(e, p.x, acc.x); acc.y = fmaf(e, p.y, acc.y);
+      acc.z = fmaf(e, p.z, acc.z); acc.w = fmaf(e, p.w, acc.w);
+    };
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i)
+      if (np + i * kNp < n) add(x[i], np + i * kNp);
+#pragma unroll 8
+    for (int j = np + kFirst * kNp; j < n; j += kNp) add(part_at(j), j);
+    if constexpr (kNp > 1) {
+      float4* sums = reinterpret_cast<float4*>(s_sums);
+      sums[np * C::kVec + v] = acc;
+      __syncthreads();
+      if (np == 0) {
+#pragma unroll
+        for (int k = 1; k < kNp; ++k) {
+          const float4 p = sums[k * C::kVec + v];
+          acc.x += p.x; acc.y += p.y; acc.z += p.z; acc.w += p.w;
+        }
+      }
+    }
+    return acc;
+  };
+  // Takes a ticket of n; true for the last.  The counter runs to n - 1 and starts again at 0: ready
+  // for the next call.  (One thread: release and acquire cover what the CTA's barriers order.)
+  auto take = [](unsigned* counter, int n) {
+    unsigned old;
+    asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(n - 1) : "memory");
+    return old == (unsigned)(n - 1);
+  };
+  // a cut segment's parts are joined at once, or in blocks first
+  auto parts_of = [&](const Segment& g, int& first) {
+    first = (int)(g.lo / per);
+    return (int)((g.hi - 1) / per) - first + 1;
+  };
+  auto block_of = [&](int first, int n, size_t& slot, int& j0) {  // the CTA's block: its parts
+    j0 = ((int)blockIdx.x - first) / kJoinBlock * kJoinBlock;
+    slot = 2 * (first + j0) + (j0 == 0 ? 1 : 0);
+    return min(kJoinBlock, n - j0);
+  };
+  if (lane == 0 && warp < 2 && s_cut[warp].nt) {  // both tickets at once
+    const Segment g = s_cut[warp];
+    int first, j0;
+    size_t slot;
+    const int n = parts_of(g, first);
+    if (n <= kJoinMost) {
+      s_last[warp] = take(ka.ticket + (size_t)g.bi * a.g + g.gi, n);
+    } else {
+      const int members = block_of(first, n, slot, j0);
+      s_last[warp] = take(ka.block_ticket + slot, members);
+    }
+  }
+  __syncthreads();
+  for (int side = 0; side < 2; ++side) {
+    const Segment g = s_cut[side];
+    if (g.nt == 0 || !s_last[side]) continue;
+    int first, j0 = 0, step = 1;
+    const int n = parts_of(g, first);
+    int count = n;
+    if (n > kJoinMost) {
+      size_t slot;
+      const int members = block_of(first, n, slot, j0);
+      const float4 acc = join(first, j0, 1, members);
+      // the block's sum takes the place of its first part, which has been read
+      if (t < C::kVec) {
+        __stcg(reinterpret_cast<float4*>(ka.part + slot * G * D) + v, acc);
+        if (v * 4 % D == 0) __stcg(ka.part_ml + slot * G + hv, make_float2(s_abort ? NAN : s_M[hv], s_z[hv]));
       }
       __syncthreads();
-      if (s_last) {
-        // part j of the segment: slot 1 of the CTA where it begins, slot 0 of the others
-        auto slot_of = [&](int j) { return (size_t)(2 * (first + j) + (j == 0 ? 1 : 0)); };
-        // kNp threads share a float4 column: each sums every kNp-th part, then they are joined.
-        // The first kFirst parts are on their way while the weights are computed.
-        constexpr int kNp = kDenseThreads / C::kVec, kFirst = 4;
-        const int v = t % C::kVec, np = t / C::kVec, hv = v * 4 / D;
-        auto part_at = [&](int j) { return __ldcg(reinterpret_cast<const float4*>(ka.part + slot_of(j) * G * D) + v); };
-        float4 x[kFirst];
-#pragma unroll
-        for (int i = 0; i < kFirst; ++i)
-          x[i] = np + i * kNp < n ? part_at(np + i * kNp) : make_float4(0.f, 0.f, 0.f, 0.f);
-        bool gone = false;
-        if (warp < G) {
-          constexpr int kMl = (kDenseCtas + 31) / 32;
-          float2 ml[kMl];
-          float M = -INFINITY, z = 0.f;
-#pragma unroll
-          for (int i = 0; i < kMl; ++i) {
-            ml[i] = lane + 32 * i < n ? __ldcg(ka.part_ml + slot_of(lane + 32 * i) * G + warp) : make_float2(-INFINITY, 0.f);
-            gone |= ml[i].x != ml[i].x;
-            M = fmaxf(M, ml[i].x);
-          }
-          M = warp_max(M);
-          const float base = M == -INFINITY ? 0.f : M;
-#pragma unroll
-          for (int i = 0; i < kMl; ++i) {
-            const float e = exp2f(ml[i].x - base);
-            if (lane + 32 * i < n) s_join[warp * n + lane + 32 * i] = e;
-            z = fmaf(e, ml[i].y, z);
-          }
-          z = warp_sum(z);
-          if (lane == 0) {
-            s_M[warp] = M;
-            s_z[warp] = z;
-          }
-        }
-        if (gone) s_abort = 1;
-        __syncthreads();
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](const float4& y, int j) {
-          const float e = s_join[hv * n + j];
-          acc.x = fmaf(e, y.x, acc.x); acc.y = fmaf(e, y.y, acc.y);
-          acc.z = fmaf(e, y.z, acc.z); acc.w = fmaf(e, y.w, acc.w);
-        };
-#pragma unroll
-        for (int i = 0; i < kFirst; ++i)
-          if (np + i * kNp < n) add(x[i], np + i * kNp);
-#pragma unroll 8
-        for (int j = np + kFirst * kNp; j < n; j += kNp) add(part_at(j), j);
-        if constexpr (kNp > 1) {
-          float4* sj = reinterpret_cast<float4*>(s_join + 1536);  // behind the weights: G n <= 1184
-          sj[np * C::kVec + v] = acc;
-          __syncthreads();
-          if (np == 0) {
-#pragma unroll
-            for (int k = 1; k < kNp; ++k) {
-              const float4 y = sj[k * C::kVec + v];
-              acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
-            }
-          }
-        }
-        if (np == 0 && !s_abort) write_row(bi, gi, v, acc, s_M[hv], s_z[hv]);
-        __syncthreads();
-      }
+      step = kJoinBlock;
+      count = (n + kJoinBlock - 1) / kJoinBlock;
+      if (t == 0) s_last[side] = take(ka.ticket + (size_t)g.bi * a.g + g.gi, count);
+      __syncthreads();
+      if (!s_last[side]) continue;
     }
-    u = ue;
+    const float4 acc = join(first, 0, step, count);
+    if (t < C::kVec && !s_abort) write_row(g.bi, g.gi, v, acc, s_M[hv], s_z[hv]);
+    __syncthreads();
   }
-  // A feeding warp that gave up has copies in flight (units stuck .. issued - 1): they land before
-  // the CTA can end.
-  if (feeds && failed)
-    for (; stuck < issued; ++stuck) {
-      const int st = (int)(stuck % C::kStages);
-      if (!(bad >> st & 1u)) tc::mbar_wait(tc::smem_u32(&s_full[group][st]), phases >> st & 1u, kDrainPolls);
-    }
 }
 
 // ---- host -------------------------------------------------------------------
@@ -735,7 +852,8 @@ DenseScratch decode_dense_scratch(int b, int h, int g, int d) {
   const size_t G = h / g;
   s.part = 0;
   s.part_ml = 2ull * kDenseCtas * G * d * 4;
-  s.ticket = s.part_ml + 2ull * kDenseCtas * G * 8;
+  s.block_ticket = s.part_ml + 2ull * kDenseCtas * G * 8;
+  s.ticket = s.block_ticket + 2ull * kDenseCtas * 4;
   s.total = s.ticket + 4ull * (b < kDenseSeqs ? b : kDenseSeqs) * g;
   return s;
 }
@@ -744,13 +862,14 @@ cudaError_t run_decode_dense(const DenseArgs& a, void* scratch, cudaStream_t st)
   const DenseScratch S = decode_dense_scratch(a.b, a.h, a.g, a.d);
   const size_t es = a.bf16 ? 2 : 4;
   DenseKernelArgs ka;
-  const int rows = a.bf16 ? DenseCfg<__nv_bfloat16, 64, 1>::kTile : DenseCfg<float, 64, 1>::kTile;
+  const int rows = 8192 / (int)(a.d * es);  // kTile
   if (!encode_pages_map(&ka.tmap_k, a.k_pages, a.d, (long long)a.n_pages * a.g, a.bf16, rows) ||
       !encode_pages_map(&ka.tmap_v, a.v_pages, a.d, (long long)a.n_pages * a.g, a.bf16, rows))
     return cudaErrorInvalidValue;
   char* w = static_cast<char*>(scratch);
   ka.part = reinterpret_cast<float*>(w + S.part);
   ka.part_ml = reinterpret_cast<float2*>(w + S.part_ml);
+  ka.block_ticket = reinterpret_cast<unsigned*>(w + S.block_ticket);
   ka.ticket = reinterpret_cast<unsigned*>(w + S.ticket);
   // sequences of one launch: their prefix sums fit shared memory, their units 32 bits
   const long long fit = ((1ll << 31) - 1) / ((long long)kDenseMaxTiles * a.g * a.max_chunks);

@@ -264,7 +264,7 @@ struct DenseArgs {
 };
 // Scratch of a dense decode: partials of the cut (sequence, KV head)s and their tickets.
 struct DenseScratch {
-  size_t part, part_ml, ticket, total;
+  size_t part, part_ml, block_ticket, ticket, total;
 };
 DenseScratch decode_dense_scratch(int b, int h, int g, int d);
 bool decode_dense_supported(int g, int max_chunks, int n_pages);

@@ -391,36 +391,60 @@ def test_dense_infinite_and_missing_logits():
             _close(out[bi], want[bi], r * mag[bi] + 1.01 * _u(out.dtype) * np.abs(want[bi]) + 1e-9, "out")
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("h,g", [(2, 2), (4, 2), (8, 2), (16, 2)])
-def test_dense_long_caches(dtype, d, h, g):
-    """Enough keys that every stage of each SM's ring is filled several times, cut at odd
-    places; against the definition in 64 bits on the GPU."""
-    lens = [60001, 333, 0, 20000, 7777]
-    t, _ = _dense_case(lens, h, g, d, dtype, seed=h + d)
-    out, lse = _dense_run(t)
-    for _ in range(3):
-        again, _ = _dense_run(t)
-        assert torch.equal(again, out)
-    want, wlse = torch.zeros(5, h, d).double(), torch.full((5, h), -math.inf).double()
-    mag, size = torch.zeros(5, h, d).double(), torch.zeros(5, h).double()
+def _dense_close_gpu(out, lse, t, lens, window=0):
+    """The same bounds against the definition in 64 bits on the GPU, for long caches.  Their sums
+    run over at most a few thousand terms at a time (units, warps, SMs): n = 4096."""
+    b, h, d = t["q"].shape
+    g = t["k_pages"].shape[1]
+    want, wlse = torch.zeros(b, h, d).double(), torch.full((b, h), -math.inf).double()
+    mag, size = torch.zeros(b, h, d).double(), torch.zeros(b, h).double()
     for bi, n in enumerate(lens):
         if n == 0:
             continue
-        pages = t["block_table"][bi, :-(-n // 64)].long()
-        for hi in range(h):
-            k, v = (t[x][pages, hi // (h // g)].reshape(-1, d)[:n].double() for x in ("k_pages", "v_pages"))
-            qr = t["q"][bi, hi].double()
-            s = k @ qr * d ** -0.5
-            p = torch.softmax(s, 0)
-            wlse[bi, hi], want[bi, hi], mag[bi, hi] = torch.logsumexp(s, 0), p @ v, p @ v.abs()
-            size[bi, hi] = (k.abs() @ qr.abs()).max() * d ** -0.5
+        lo = max(0, ((n - 1) // 64 + 1 - window // 64) * 64) if window else 0
+        pages = t["block_table"][bi, lo // 64:-(-n // 64)].long()
+        for gi in range(g):
+            k, v = (t[x][pages, gi].reshape(-1, d)[:n - lo].double() for x in ("k_pages", "v_pages"))
+            rows = slice(gi * (h // g), (gi + 1) * (h // g))
+            q = t["q"][bi, rows].double()
+            s = q @ k.T * d ** -0.5
+            p = torch.softmax(s, -1)
+            wlse[bi, rows], want[bi, rows], mag[bi, rows] = torch.logsumexp(s, -1).cpu(), (p @ v).cpu(), (p @ v.abs()).cpu()
+            size[bi, rows] = ((q.abs() @ k.abs().T).amax(-1) * d ** -0.5).cpu()
     want, wlse, mag, size = (x.numpy() for x in (want, wlse, mag, size))
-    # sums run over at most a few thousand terms at a time (16-key slices, warps, SMs): n = 4096
     r = 2 * d * 2.0 ** -23 * size + 2.0 ** -16 + 4096 * 2.0 ** -23
     _close(out, want, r[..., None] * mag + _u(out.dtype) * (np.abs(want) + r[..., None] * mag), "out")
     _close(lse, wlse, r + 2.0 ** -22 * np.abs(np.where(np.isfinite(wlse), wlse, 0)), "lse")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("h,g,lens", [
+    (2, 2, [60001, 333, 0, 20000, 7777]), (4, 2, [60001, 333, 0, 20000, 7777]), (8, 2, [60001, 333, 0, 20000, 7777]),
+    (16, 2, [60001, 333, 0, 20000, 7777]),
+    (8, 1, [150001]), (1, 1, [150001]), (2, 1, [99, 130000, 64]),  # one head cut between more than 32 SMs
+])
+def test_dense_long_caches(dtype, d, h, g, lens):
+    """Enough keys that every stage of each SM's rings is filled several times, cut at odd
+    places; the same bits each time."""
+    t, _ = _dense_case(lens, h, g, d, dtype, seed=h + d)
+    out, lse = _dense_run(t)
+    for _ in range(3):
+        again, again_lse = _dense_run(t)
+        assert torch.equal(again, out) and torch.equal(again_lse, lse)
+    _dense_close_gpu(out, lse, t, lens)
+
+
+@pytest.mark.parametrize("b,h,g,d,most,window", [(70, 8, 2, 128, 700, 0), (300, 4, 4, 64, 300, 0),
+                                                 (1100, 2, 1, 64, 200, 0), (90, 16, 2, 64, 3000, 256)])
+def test_dense_batches_of_short_sequences(b, h, g, d, most, window):
+    """Many (sequence, KV head)s per warp; more sequences than one launch takes."""
+    rng = np.random.RandomState(b)
+    lens = [0 if i % 11 == 3 else int(rng.randint(1, most)) for i in range(b)]
+    for dtype in ("bf16", "f32"):
+        t, _ = _dense_case(lens, h, g, d, dtype, seed=b, needles=False)
+        out, lse = _dense_run(t, window=window)
+        _dense_close_gpu(out, lse, t, lens, window)
 
 
 def test_dense_every_length_of_a_ragged_batch():
