@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -53,15 +54,6 @@ def _shape_of(*key):
             _SHAPES.clear()
         s = _SHAPES[key] = make_shape(*key)
     return s
-
-
-class Rows(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
-                ("token_stride", ctypes.c_int64)]
-
-
-class Rope(ctypes.Structure):
-    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 _lib = None
@@ -525,6 +517,10 @@ def _own_workspace(shape, op, device, ws):
     return ws
 
 
+def _dtype_of(shape):
+    return torch.bfloat16 if shape.dtype == HILS_BF16 else torch.float32
+
+
 def _dense_shape(batch, heads_q, heads_kv, head_dim, max_chunks, dtype, scale=None, window=0):
     if max_chunks * 64 >= 1 << 31:
         raise ValueError("max_chunks * 64 must stay below 2**31")
@@ -561,24 +557,31 @@ def _empty(shape, dtype, t, stream):
         return torch.empty(shape, dtype=dtype, device=t.device)
 
 
-# hils_rows and hils_rope structs of a call, packed into one array of 8-byte words (a hils_rows
-# is 4 words; a hils_rope 2: the pointer, then rotary_dim | interleaved << 32).
-_Words = {n: ctypes.c_int64 * n for n in (8, 10, 16, 18)}
+# hils_rows and hils_rope structs as bytes, which ctypes passes by address: several times
+# cheaper to make than ctypes structures.
+_pack_rows = struct.Struct("4q").pack
+_pack_rope = struct.Struct("qii").pack
 
 
-def _rope_words(inv_freq, interleaved, d):
+def _rope_bytes(inv_freq, interleaved, d):
     if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous():
         raise TypeError("inv_freq must be a contiguous fp32 vector")
     r = 2 * inv_freq.numel()
     if r == 0 or r > d or r % 16:
         raise ValueError(f"inv_freq must have a multiple of 8 entries, at most head_dim / 2; got {r // 2}")
-    return inv_freq.data_ptr(), r | (1 << 32 if interleaved else 0)
+    return _pack_rope(inv_freq.data_ptr(), r, 1 if interleaved else 0)
 
 
-def _last_contiguous(*named):
-    for name, t in named:
+def _rows4(t):
+    """[b, heads, n, d] as hils_rows."""
+    st = t.stride()
+    return _pack_rows(t.data_ptr(), st[0], st[1], st[2])
+
+
+def _contiguous_rows(*ts):
+    for t in ts:
         if t is not None and t.stride(-1) != 1:
-            raise ValueError(f"{name}: the last dimension must be contiguous")
+            raise ValueError("the last dimension of q, k, v and their outputs must be contiguous")
 
 
 def check_rotate_args(q, inv_freq, k=None, positions=None, q_out=None, k_out=None):
@@ -601,7 +604,7 @@ def check_rotate_args(q, inv_freq, k=None, positions=None, q_out=None, k_out=Non
             _expect(k_out, k.shape, (q.dtype if q_out is None else q_out.dtype,), "k_out")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _last_contiguous(("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out))
+    _contiguous_rows(q, k, q_out, k_out)
     _same_device(q, inv_freq, k, positions, q_out, k_out)
     if positions is None:
         return 0
@@ -625,27 +628,44 @@ def rotate(q, inv_freq, k=None, positions=None, inverse=False, interleaved=False
     dq and dk) to those of the unrotated ones.  The tensors may have any strides whose rows are
     contiguous and 16-byte aligned; an output may be its input (in place), and may be bf16 or
     fp32 whatever the input is."""
-    pstride = check_rotate_args(q, inv_freq, k, positions, q_out, k_out)
-    b, h, n, d = q.shape
+    qs, dt, dev = q.shape, q.dtype, q.get_device()
+    # the call as it mostly comes, in one expression; any other goes through the full check,
+    # which says what is wrong
+    if (len(qs) == 4 and dt in _FLOATS and inv_freq is not None and inv_freq.get_device() == dev and
+            (positions is None or positions.shape == (qs[0], qs[2]) and positions.dtype is torch.int32 and
+             positions.get_device() == dev and positions.is_contiguous()) and k is not None and k.dtype is dt and k.get_device() == dev and
+            k.shape[2:] == qs[2:] and k.shape[0] == qs[0] and k.stride(-1) == 1 and q.stride(-1) == 1 and
+            (q_out is None or q_out.shape == qs and q_out.dtype is dt and q_out.get_device() == dev and
+             q_out.stride(-1) == 1) and
+            (k_out is None or q_out is not None and k_out.shape == k.shape and k_out.dtype is dt and
+             k_out.get_device() == dev and k_out.stride(-1) == 1)):
+        pstride = 0 if positions is None else qs[2]
+    else:
+        pstride = check_rotate_args(q, inv_freq, k, positions, q_out, k_out)
+    b, h, n, d = qs
     if q_out is None:
         q_out = _empty(q.shape, q.dtype, q, stream)
     if k is not None and k_out is None:
         k_out = _empty(k.shape, q_out.dtype, q, stream)
-    words = _rope_words(inv_freq, interleaved, d)
-    qs, os = q.stride(), q_out.stride()
-    words += (q.data_ptr(), qs[0], qs[1], qs[2], q_out.data_ptr(), os[0], os[1], os[2])
-    g = h
-    if k is not None:
-        g = k.shape[1]
-        qs, os = k.stride(), k_out.stride()
-        words += (k.data_ptr(), qs[0], qs[1], qs[2], k_out.data_ptr(), os[0], os[1], os[2])
+    rope = _rope_bytes(inv_freq, interleaved, d)
+    g = h if k is None else k.shape[1]
     if b * n * h * g:
-        w = _Words[len(words)](*words)
-        at = ctypes.addressof(w)
-        _launch(lib().hils_rotate, "hils_rotate", q, stream, _shape_of(b, h, g, d, n, 0, _dt(q)), at + 16,
-                None if k is None else at + 80, at, None if positions is None else positions.data_ptr(), pstride,
-                1 if inverse else 0, at + 48, None if k is None else at + 112, _dt(q_out))
+        _launch(lib().hils_rotate, "hils_rotate", q, stream, _shape_of(b, h, g, d, n, 0, _dt(q)), _rows4(q),
+                None if k is None else _rows4(k), rope, None if positions is None else positions.data_ptr(), pstride,
+                1 if inverse else 0, _rows4(q_out), None if k is None else _rows4(k_out), _dt(q_out))
     return q_out if k is None else (q_out, k_out)
+
+
+def _rows_single(t):
+    """[b, heads, d], one token each, as hils_rows."""
+    st = t.stride()
+    return _pack_rows(t.data_ptr(), st[0], st[1], 0)
+
+
+def _rows_packed(t):
+    """[tokens, heads, d] as hils_rows."""
+    st = t.stride()
+    return _pack_rows(t.data_ptr(), 0, st[1], st[0])
 
 
 def append_slots(batch, tokens):
@@ -659,7 +679,7 @@ def check_append_args(shape, k, v, k_pages, v_pages, block_table, max_chunks, se
     """The tensors of an append against the shape (see Append.__call__).  Alignment and
     overlaps are checked by hils_append_paged."""
     b, h, g, d = shape.batch, shape.heads_q, shape.heads_kv, shape.head_dim
-    dts = (torch.bfloat16 if shape.dtype == HILS_BF16 else torch.float32,)
+    dts = (_dtype_of(shape),)
     if k.dim() == 3:
         n = tokens = k.shape[0]
         rows, qrows = (n, g, d), (n, h, d)
@@ -694,7 +714,7 @@ def check_append_args(shape, k, v, k_pages, v_pages, block_table, max_chunks, se
         raise ValueError("q_out without q")
     if full_pages is not None:
         _expect(full_pages, (append_slots(b, tokens),), (torch.int32,), "full_pages")
-    _last_contiguous(("k", k), ("v", v), ("q", q), ("q_out", q_out))
+    _contiguous_rows(k, v, q, q_out)
     _same_device(k, v, q, q_out, k_pages, v_pages, block_table, seq_lens, cu_new, new_lens, full_pages)
 
 
@@ -708,9 +728,10 @@ class Append:
         self.max_chunks = max_chunks
         self.shape = _dense_shape(batch, heads_q, heads_kv, head_dim, max_chunks, dtype)
         self.inv_freq = inv_freq
-        self.rope = None if inv_freq is None else _Words[10](*_rope_words(inv_freq, interleaved, head_dim))
+        self.rope = None if inv_freq is None else _rope_bytes(inv_freq, interleaved, head_dim)
         self.ws = _own_workspace(self.shape, OP_APPEND, device, ws)
         _same_device(self.ws, inv_freq)
+        self.dev, self.dtype = self.ws.get_device(), _dtype_of(self.shape)
 
     def __call__(self, k, v, k_pages, v_pages, block_table, seq_lens, q=None, q_out=None, cu_new=None, new_lens=None,
                  full_pages=None, stream=None):
@@ -723,29 +744,41 @@ class Append:
         seq_lens [b] int32 are the lengths after the call.  full_pages: int32
         [append_slots(b, tokens)], receives the pages filled by the call, else -1: it can go to
         summarize_paged as it is.  q_out may be q itself."""
-        s = self.shape
-        check_append_args(s, k, v, k_pages, v_pages, block_table, self.max_chunks, seq_lens, q, q_out, cu_new,
-                          new_lens, full_pages)
-        _same_device(k, self.ws)
+        s, dt, dev, i32 = self.shape, self.dtype, self.dev, torch.int32
+        ks, ps = k.shape, k_pages.shape
+        b, h, g, d = s.batch, s.heads_q, s.heads_kv, s.head_dim
+        # packed tokens as they mostly come, in one expression; any other call goes through the
+        # full check, which says what is wrong
+        if not (len(ks) == 3 and new_lens is None and ks[1] == g and ks[2] == d and k.dtype is dt and v.dtype is dt and
+                v.shape == ks and k.get_device() == dev and v.get_device() == dev and
+                k.stride(-1) == 1 and v.stride(-1) == 1 and
+                (ks[0] == b if cu_new is None else
+                 cu_new.shape == (b + 1,) and cu_new.dtype is i32 and cu_new.get_device() == dev) and
+                len(ps) == 4 and ps[1] == g and ps[2] == 64 and ps[3] == d and v_pages.shape == ps and
+                k_pages.dtype is dt and v_pages.dtype is dt and
+                k_pages.get_device() == dev and v_pages.get_device() == dev and
+                block_table.shape == (b, self.max_chunks) and block_table.dtype is i32 and
+                block_table.get_device() == dev and
+                seq_lens.shape == (b,) and seq_lens.dtype is i32 and seq_lens.get_device() == dev and
+                (q_out is None if q is None else
+                 q.shape == (ks[0], h, d) and q.dtype is dt and q.get_device() == dev and q.stride(-1) == 1 and
+                 (q_out is None or q_out.shape == q.shape and q_out.dtype is dt and q_out.get_device() == dev and
+                  q_out.stride(-1) == 1)) and
+                (full_pages is None or full_pages.shape == (append_slots(b, ks[0]),) and full_pages.dtype is i32 and
+                 full_pages.get_device() == dev)):
+            check_append_args(s, k, v, k_pages, v_pages, block_table, self.max_chunks, seq_lens, q, q_out, cu_new,
+                              new_lens, full_pages)
+            _same_device(k, self.ws)
         if q is not None and q_out is None:
             q_out = _empty(q.shape, q.dtype, k, stream)
-        packed = k.dim() == 3
-
-        def words(t):
-            st = t.stride()
-            if not packed:
-                return t.data_ptr(), st[0], st[1], st[2]
-            # one row per token; without cu_new the tokens are the batch, one each
-            return (t.data_ptr(), 0, st[1], st[0]) if cu_new is not None else (t.data_ptr(), st[0], st[1], 0)
-
-        w = words(k) + words(v)
-        if q is not None:
-            w += words(q) + words(q_out)
-        w = _Words[len(w)](*w)
-        at = ctypes.addressof(w)
-        n_new = k.shape[2] if not packed else 1 if cu_new is None else k.shape[0]
-        _launch(lib().hils_append_paged, "hils_append_paged", k, stream, s, at, at + 32,
-                None if q is None else at + 64, None if q is None else at + 96, n_new, _at(cu_new), _at(new_lens),
+        if len(ks) == 4:
+            n_new, rows = ks[2], _rows4
+        elif cu_new is None:  # one token per sequence: [b, heads, 1, d]
+            n_new, rows = 1, _rows_single
+        else:
+            n_new, rows = ks[0], _rows_packed
+        _launch(lib().hils_append_paged, "hils_append_paged", k, stream, s, rows(k), rows(v),
+                None if q is None else rows(q), None if q is None else rows(q_out), n_new, _at(cu_new), _at(new_lens),
                 _at(seq_lens), _at(block_table), self.max_chunks, k_pages.shape[0], self.rope, _at(k_pages),
                 _at(v_pages), _at(full_pages), _at(self.ws), self.ws.numel())
         return q_out
@@ -772,7 +805,7 @@ def check_dense_args(shape, q, k_pages, v_pages, block_table, max_chunks, seq_le
     """The tensors of a dense decode against the shape: q [b,h,d]; k/v pages [P,g,64,d] in q's
     dtype; block_table [b, max_chunks] and seq_lens [b] int32; out like q; lse [b,h] fp32."""
     b, h, d = shape.batch, shape.heads_q, shape.head_dim
-    dts = (torch.bfloat16 if shape.dtype == HILS_BF16 else torch.float32,)
+    dts = (_dtype_of(shape),)
     _expect(q, (b, h, d), dts, "q")
     pages = (k_pages.shape[0] if k_pages.dim() == 4 else -1, shape.heads_kv, 64, d)
     _expect(k_pages, pages, dts, "k_pages")
@@ -796,11 +829,25 @@ class DenseDecode:
         self.max_chunks = max_chunks
         self.shape = _dense_shape(batch, heads_q, heads_kv, head_dim, max_chunks, dtype, scale, window)
         self.ws = _own_workspace(self.shape, OP_DECODE_DENSE, device, ws)
+        self.dev, self.dtype = self.ws.get_device(), _dtype_of(self.shape)
 
     def __call__(self, q, k_pages, v_pages, block_table, seq_lens, out=None, lse=None, stream=None):
         """out [b,h,d] (q's dtype); lse, if given (fp32 [b,h]), receives log sum exp(logit)."""
-        check_dense_args(self.shape, q, k_pages, v_pages, block_table, self.max_chunks, seq_lens, out, lse)
-        _same_device(q, self.ws)
+        s, dt, dev, i32 = self.shape, self.dtype, self.dev, torch.int32
+        b, qs, ps = s.batch, q.shape, k_pages.shape
+        # in one expression; where it does not hold, the full check says what is wrong
+        if not (qs == (b, s.heads_q, s.head_dim) and q.dtype is dt and q.get_device() == dev and
+                len(ps) == 4 and ps[1] == s.heads_kv and ps[2] == 64 and ps[3] == s.head_dim and
+                v_pages.shape == ps and k_pages.dtype is dt and v_pages.dtype is dt and
+                k_pages.get_device() == dev and v_pages.get_device() == dev and
+                block_table.shape == (b, self.max_chunks) and block_table.dtype is i32 and
+                block_table.get_device() == dev and
+                seq_lens.shape == (b,) and seq_lens.dtype is i32 and seq_lens.get_device() == dev and
+                (out is None or out.shape == qs and out.dtype is dt and out.get_device() == dev) and
+                (lse is None or lse.shape == (b, s.heads_q) and lse.dtype is torch.float32 and
+                 lse.get_device() == dev)):
+            check_dense_args(s, q, k_pages, v_pages, block_table, self.max_chunks, seq_lens, out, lse)
+            _same_device(q, self.ws)
         if out is None:
             out = _empty(q.shape, q.dtype, q, stream)
         _launch(lib().hils_decode_dense, "hils_decode_dense", q, stream, self.shape, _at(q), _at(k_pages),

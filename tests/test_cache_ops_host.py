@@ -8,7 +8,7 @@ import torch
 
 import chunk_wise_hierarchical_b200 as hils
 from chunk_wise_hierarchical_b200 import _abi
-from chunk_wise_hierarchical_b200._abi import (HILS_BF16, HILS_F32, Rope, Rows, check_append_args, check_dense_args,
+from chunk_wise_hierarchical_b200._abi import (HILS_BF16, HILS_F32, check_append_args, check_dense_args,
                                                check_rotate_args, make_shape)
 from oracle import cache_oracle as CO
 from oracle import hils_oracle as O
@@ -16,6 +16,15 @@ from oracle import hils_oracle as O
 BF = torch.bfloat16
 P_ = ctypes.c_void_p
 FAKE = P_(1 << 20)  # never dereferenced
+
+
+class Rows(ctypes.Structure):  # hils_rows
+    _fields_ = [("data", P_), ("batch_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64)]
+
+
+class Rope(ctypes.Structure):  # hils_rope
+    _fields_ = [("inv_freq", P_), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 # ---- the oracle -------------------------------------------------------------
@@ -51,6 +60,23 @@ def test_oracle_dense_decode_is_the_last_row_of_dense_attention():
 
 
 # ---- the binding's checks ---------------------------------------------------
+# On the host a call whose arguments are right goes as far as its launch, which then misses the
+# GPU: "CUDA device".  A refusal says something else, and comes before.
+def _right(call, *args, **kw):
+    with pytest.raises(ValueError, match="CUDA device"):
+        call(*args, **kw)
+
+
+def _refused(call, *args, **kw):
+    with pytest.raises((ValueError, TypeError)) as e:
+        call(*args, **kw)
+    assert "CUDA device" not in str(e.value)
+
+
+def _ws(n=1 << 22):
+    return torch.zeros(n, dtype=torch.uint8)
+
+
 B, H, G, N, D = 2, 8, 2, 70, 64
 
 
@@ -85,6 +111,17 @@ def test_rotate_refuses(kw):
     a.update(kw)
     with pytest.raises((ValueError, TypeError)):
         check_rotate_args(**a)
+    _refused(hils.rotate, **a)
+    if "k" not in kw and "k_out" not in kw:
+        _refused(hils.rotate, k=torch.zeros(B, G, N, D, dtype=BF), **a)
+
+
+def test_rotate_takes_what_is_right_as_far_as_the_device():
+    q, k, f = torch.zeros(B, H, N, D, dtype=BF), torch.zeros(B, G, N, D, dtype=BF), torch.ones(16)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    for kw in (dict(), dict(k=k), dict(k=k, positions=i(B, N)), dict(k=k, positions=i(N)), dict(k=k, q_out=q, k_out=k),
+               dict(k=k, q_out=q.float(), k_out=k.float()), dict(k=k, k_out=k.clone())):
+        _right(hils.rotate, q, f, **kw)
 
 
 def test_rotate_refuses_overlapping_and_expanded_outputs():
@@ -116,7 +153,20 @@ def test_rotate_refuses_overlapping_and_expanded_outputs():
                                torch.ones(4, 4), torch.ones(32)[::2]])
 def test_rope_refuses(f):
     with pytest.raises((ValueError, TypeError)):
-        _abi._rope_words(f, False, 64)
+        _abi._rope_bytes(f, False, 64)
+
+
+def test_structs_are_packed_as_declared():
+    t = torch.zeros(2, 3, 5, 64, dtype=BF)
+    r = Rows.from_buffer_copy(_abi._rows4(t))
+    assert (r.data, r.batch_stride, r.head_stride, r.token_stride) == (t.data_ptr(), 960, 320, 64)
+    r = Rows.from_buffer_copy(_abi._rows_packed(t[0]))
+    assert (r.head_stride, r.token_stride) == (64, 320)
+    r = Rows.from_buffer_copy(_abi._rows_single(t[0]))
+    assert (r.batch_stride, r.head_stride, r.token_stride) == (320, 64, 0)
+    f = torch.ones(24)
+    o = Rope.from_buffer_copy(_abi._rope_bytes(f, True, 64))
+    assert (o.inv_freq, o.rotary_dim, o.interleaved) == (f.data_ptr(), 48, 1)
 
 
 def test_rows_need_contiguous_last_dimension():
@@ -145,6 +195,14 @@ def test_append_arguments():
                                          new_lens=torch.zeros(B, dtype=torch.int32),
                                          full_pages=torch.zeros(B + 80 // 64, dtype=torch.int32)))
     check_append_args(make_shape(B, H, G, D, 3 * 64, 0, HILS_F32), **_append_args(torch.float32))
+    call = hils.Append(B, H, G, D, 3, BF, inv_freq=torch.ones(16), ws=_ws())
+    for a in (_append_args(), _append_args(q_out=z(9, H, D)), _append_args(q=None), _append_args(full_pages=None),
+              _append_args(k=z(B, G, D), v=z(B, G, D), q=z(B, H, D), cu_new=None,
+                           full_pages=torch.zeros(B, dtype=torch.int32)),
+              _append_args(k=z(B, G, 40, D), v=z(B, G, 40, D), q=z(B, H, 40, D), cu_new=None,
+                           full_pages=torch.zeros(B + 80 // 64, dtype=torch.int32))):
+        a.pop("max_chunks")
+        _right(call, **a)
 
 
 @pytest.mark.parametrize("kw", [
@@ -169,6 +227,9 @@ def test_append_arguments():
 def test_append_refuses(kw):
     with pytest.raises((ValueError, TypeError)):
         check_append_args(make_shape(B, H, G, D, 3 * 64, 0, HILS_BF16), **_append_args(**kw))
+    a = _append_args(**kw)
+    a.pop("max_chunks")
+    _refused(hils.Append(B, H, G, D, 3, BF, ws=_ws()), **a)
 
 
 def _dense_args(**kw):
@@ -191,6 +252,21 @@ def test_dense_refuses(kw):
     check_dense_args(sh, **_dense_args())
     with pytest.raises((ValueError, TypeError)):
         check_dense_args(sh, **_dense_args(**kw))
+    call = hils.DenseDecode(B, H, G, D, 3, BF, ws=_ws())
+    a = _dense_args(**kw)
+    a.pop("max_chunks")
+    _refused(call, **a)
+    a = _dense_args(out=torch.zeros(B, H, D, dtype=BF), lse=torch.zeros(B, H))
+    a.pop("max_chunks")
+    _right(call, **a)
+
+
+def test_a_workspace_of_the_caller_is_checked():
+    need = _abi.workspace_size(make_shape(B, H, G, D, 3 * 64, 0, HILS_BF16), hils.OP_DECODE_DENSE)
+    hils.DenseDecode(B, H, G, D, 3, BF, ws=_ws(need))
+    for ws in (_ws(need - 1), torch.zeros(need, dtype=torch.int32), _ws(2 * need)[::2]):
+        with pytest.raises(ValueError):
+            hils.DenseDecode(B, H, G, D, 3, BF, ws=ws)
 
 
 def test_cache_calls_refuse_cpu_tensors_and_lengths_beyond_int32():
