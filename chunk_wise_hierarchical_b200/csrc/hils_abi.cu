@@ -523,6 +523,7 @@ hils_status hils_rotate(const hils_shape* s, const hils_rows* q, const hils_rows
   if (position_stride < 0) return HILS_ERR_INVALID_ARG;
   if ((st = check_rope(rope, s->head_dim)) != HILS_OK) return st;
   if ((size_t)s->batch * s->seq_len == 0) return HILS_OK;
+  if ((long long)s->batch * s->seq_len > 0x7fffffffll) return HILS_ERR_UNSUPPORTED;
   {
     const long long nb = s->batch, nt = s->seq_len;
     const size_t ei = elem_size(s->dtype), eo = elem_size(out_dtype);

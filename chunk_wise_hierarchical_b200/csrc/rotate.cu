@@ -16,9 +16,10 @@
 // loads, the products and two stores.  The tokens of the whole batch are numbered in a row, and
 // a CTA takes kRotThreads / (units per row) of them: short sequences fill it as long ones do.
 // Loads and stores are marked as streaming (nothing is read twice): reads that stayed in L2
-// pushed half-written output lines out of it (345M prefill shape, q and k, slices of a fused
-// projection: 55 -> 47 us, 268 MB, 5.7 TB/s; fp32 gradients of the 16K training shape 167 us,
-// 6.4 TB/s; 23K prompt tokens of the 7B shape appended in 81 us, 6.0 TB/s).
+// pushed half-written output lines out of it (345M prefill shape: 55 -> 47 us).  Measured:
+// q and k of the 345M prefill shape, slices of a fused projection, 44 us (268 MB, 6.1 TB/s);
+// fp32 gradients of the 16K training shape 165 us (1.07 GB, 6.5 TB/s); 20K prompt tokens of the
+// 7B shape appended in 81 us (490 MB, 6.1 TB/s); one token for each of 64 sequences 3.9 us.
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -108,8 +109,9 @@ struct Turns {
 
 // Turns one unit's two pieces and stores them.
 template <typename Tin, typename Tout, int E = Unit<Tin>::E>
-__device__ __forceinline__ void turn_unit(const uint4& r0, const uint4& r1, const Turns<E>& t, Tout* d0, Tout* d1) {
-  if (sizeof(Tin) == sizeof(Tout) && t.how == kCopied) {  // bit for bit
+__device__ __forceinline__ void turn_unit(const uint4& r0, const uint4& r1, const Turns<E>& t, int how, Tout* d0,
+                                          Tout* d1) {
+  if (sizeof(Tin) == sizeof(Tout) && how == kCopied) {  // bit for bit
     __stcs(reinterpret_cast<uint4*>(d0), r0);
     __stcs(reinterpret_cast<uint4*>(d1), r1);
     return;
@@ -117,7 +119,7 @@ __device__ __forceinline__ void turn_unit(const uint4& r0, const uint4& r1, cons
   float a[E], b[E];
   unpack<Tin>(r0, a);
   unpack<Tin>(r1, b);
-  if (t.how == kAdjacent) {
+  if (how == kAdjacent) {
 #pragma unroll
     for (int i = 0; i < E; i += 2) {
       const float2 w0 = t.w[i / 2], w1 = t.w[E / 2 + i / 2];
@@ -127,7 +129,7 @@ __device__ __forceinline__ void turn_unit(const uint4& r0, const uint4& r1, cons
       b[i] = x1 * w1.x - y1 * w1.y;
       b[i + 1] = y1 * w1.x + x1 * w1.y;
     }
-  } else if (t.how == kHalves) {
+  } else if (how == kHalves) {
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const float x = a[i], y = b[i];
@@ -139,8 +141,30 @@ __device__ __forceinline__ void turn_unit(const uint4& r0, const uint4& r1, cons
   store<Tout>(d1, b);
 }
 
+// One unit of n heads: head k lies at src + k ss and goes to dst + k ds.
+template <typename Tin, typename Tout, int E = Unit<Tin>::E>
+__device__ __forceinline__ void turn_heads(const Tin* src, long long ss, Tout* dst, long long ds, int n, int o0, int o1,
+                                           const Turns<E>& t, int how) {
+  src += o0;
+  dst += o0;
+  const int step = o1 - o0;
+  for (; n > 0; n -= kRotHeads, src += kRotHeads * ss, dst += kRotHeads * ds) {
+    uint4 r0[kRotHeads], r1[kRotHeads];
+#pragma unroll
+    for (int k = 0; k < kRotHeads; ++k) {
+      if (k < n) {
+        r0[k] = __ldcs(reinterpret_cast<const uint4*>(src + k * ss));
+        r1[k] = __ldcs(reinterpret_cast<const uint4*>(src + k * ss + step));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRotHeads; ++k)
+      if (k < n) turn_unit<Tin, Tout>(r0[k], r1[k], t, how, dst + k * ds, dst + k * ds + step);
+  }
+}
+
 // Heads per CTA.  One block of all heads computes the angles once but leaves 1.4 waves of CTAs
-// at the 345M prefill shape (80 us there, 47 us with blocks of 8; blocks of 4: 51 us).
+// at the 345M prefill shape (80 us there; blocks of 16, 8 and 4 heads: 46, 44 and 48 us).
 int pick_heads(long long token_blocks, int heads) {
   int hb = heads;
   auto ctas = [&] { return token_blocks * ((heads + hb - 1) / hb); };
@@ -160,40 +184,25 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(RotateArgs a) {
   const int n_hb = (heads + a.head_block - 1) / a.head_block;
   const int h0 = (int)(blockIdx.x % n_hb) * a.head_block, h1 = min(heads, h0 + a.head_block);
   const int u = threadIdx.x % U;
-  const long long row = (long long)(blockIdx.x / n_hb) * (kRotThreads / U) + threadIdx.x / U;
-  if (row >= (long long)a.b * a.n) return;
-  const int bi = (int)(row / a.n), i = (int)(row % a.n);
+  const unsigned row = blockIdx.x / n_hb * (kRotThreads / U) + threadIdx.x / U;  // b n < 2^31
+  if (row >= (unsigned)a.b * (unsigned)a.n) return;
+  const int bi = (int)(row / (unsigned)a.n), i = (int)(row % (unsigned)a.n);
   int o0, o1;
   unit_offsets<E>(u, a.rot, a.interleaved, o0, o1);
-  const Tin* src[2];
-  Tout* dst[2];
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    src[w] = static_cast<const Tin*>(a.in[w].data) + bi * a.in[w].batch_stride + i * a.in[w].token_stride;
-    dst[w] = static_cast<Tout*>(a.out[w].data) + bi * a.out[w].batch_stride + i * a.out[w].token_stride;
-  }
   const int pos = a.positions ? a.positions[bi * a.position_stride + i] : i;
   Turns<E> t;
   t.set(pos, a.inv_freq, u, a.rot, a.interleaved, a.inverse);
-  for (int h = h0; h < h1; h += kRotHeads) {
-    uint4 r0[kRotHeads], r1[kRotHeads];
-#pragma unroll
-    for (int k = 0; k < kRotHeads; ++k) {
-      const int hh = h + k, w = hh >= a.heads[0];
-      if (hh < h1) {
-        const Tin* p = src[w] + (hh - (w ? a.heads[0] : 0)) * a.in[w].head_stride;
-        r0[k] = __ldcs(reinterpret_cast<const uint4*>(p + o0));
-        r1[k] = __ldcs(reinterpret_cast<const uint4*>(p + o1));
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kRotHeads; ++k) {
-      const int hh = h + k, w = hh >= a.heads[0];
-      if (hh < h1) {
-        Tout* p = dst[w] + (hh - (w ? a.heads[0] : 0)) * a.out[w].head_stride;
-        turn_unit<Tin, Tout>(r0[k], r1[k], t, p + o0, p + o1);
-      }
-    }
+#pragma unroll 1
+  for (int w = 0; w < 2; ++w) {  // the block's heads of q, then those of k
+    const int lo = max(h0 - (w ? a.heads[0] : 0), 0), hi = min(h1 - (w ? a.heads[0] : 0), a.heads[w]);
+    if (lo >= hi) continue;
+    const Rows& in = a.in[w];
+    const Rows& out = a.out[w];
+    turn_heads<Tin, Tout>(
+        static_cast<const Tin*>(in.data) + bi * in.batch_stride + i * in.token_stride + lo * in.head_stride,
+        in.head_stride,
+        static_cast<Tout*>(out.data) + bi * out.batch_stride + i * out.token_stride + lo * out.head_stride,
+        out.head_stride, hi - lo, o0, o1, t, t.how);
   }
 }
 
@@ -279,10 +288,10 @@ __global__ void __launch_bounds__(kRotThreads) append_kernel(AppendArgs a, int n
   const int n_hb = (heads + a.head_block - 1) / a.head_block;
   const int h0 = (int)(blockIdx.x % n_hb) * a.head_block, h1 = min(heads, h0 + a.head_block);
   const int u = t % U;
-  const long long row = (long long)(blockIdx.x / n_hb) * (kRotThreads / U) + t / U;
-  if (row >= (packed ? (long long)a.n_new : (long long)a.b * a.n_new)) return;
-  const int bi = packed ? find_seq(cu, a.b, (int)row) : (int)(row / a.n_new);
-  const int i = packed ? (int)row - cu[bi] : (int)(row % a.n_new);
+  const unsigned row = blockIdx.x / n_hb * (kRotThreads / U) + t / U;  // fewer than 2^31 rows
+  if (row >= (packed ? (unsigned)a.n_new : (unsigned)a.b * (unsigned)a.n_new)) return;
+  const int bi = packed ? find_seq(cu, a.b, (int)row) : (int)(row / (unsigned)a.n_new);
+  const int i = packed ? (int)row - cu[bi] : (int)(row % (unsigned)a.n_new);
   const int n = packed ? cu[bi + 1] - cu[bi] : a.new_lens ? min(a.new_lens[bi], a.n_new) : a.n_new;
   if (i < 0 || i >= n) return;  // padding
   const long long pos = (long long)a.seq_lens[bi] - n + i;
@@ -295,49 +304,31 @@ __global__ void __launch_bounds__(kRotThreads) append_kernel(AppendArgs a, int n
   }
   if (pos < 0) return;
 
-  const long long bs = packed ? 0 : bi, is = packed ? row : i;
+  const long long bs = packed ? 0 : bi, is = packed ? (long long)row : i;
   const int rot = h0 < a.h + a.g ? a.rot : 0;  // a block of values needs no angles
   Turns<E> w;
   w.set((int)pos, a.inv_freq, u, rot, a.interleaved, false);
   int o0, o1;
   unit_offsets<E>(u, a.rot, a.interleaved, o0, o1);
   const size_t cell = ((size_t)(page < 0 ? 0 : page) * a.g * kChunk + (size_t)(pos % kChunk)) * D;  // of head 0
-  // where head hh comes from and goes to
-  auto source = [&](int hh) {
-    const bool is_q = hh < a.h, is_k = !is_q && hh < a.h + a.g;
-    const Rows& R = is_q ? a.q : is_k ? a.k : a.v;
-    return static_cast<const T*>(R.data) + bs * R.batch_stride + (hh - (is_q ? 0 : is_k ? a.h : a.h + a.g)) * R.head_stride +
-           is * R.token_stride;
-  };
-  auto target = [&](int hh) {
-    if (hh < a.h)
-      return static_cast<T*>(a.q_out.data) + bs * a.q_out.batch_stride + hh * a.q_out.head_stride + is * a.q_out.token_stride;
-    const bool is_k = hh < a.h + a.g;
-    return static_cast<T*>(is_k ? a.k_pages : a.v_pages) + cell + (size_t)(hh - (is_k ? a.h : a.h + a.g)) * kChunk * D;
-  };
-  for (int h = h0; h < h1; h += kRotHeads) {
-    uint4 r0[kRotHeads], r1[kRotHeads];
-#pragma unroll
-    for (int k = 0; k < kRotHeads; ++k) {
-      if (h + k < h1) {
-        const T* p = source(h + k);
-        r0[k] = __ldcs(reinterpret_cast<const uint4*>(p + o0));
-        r1[k] = __ldcs(reinterpret_cast<const uint4*>(p + o1));
-      }
+#pragma unroll 1
+  for (int part = 0; part < 3; ++part) {  // the block's heads of q, of k and of v
+    const int base = part == 0 ? 0 : part == 1 ? a.h : a.h + a.g, count = part == 0 ? a.h : a.g;
+    const int lo = max(h0 - base, 0), hi = min(h1 - base, count);
+    if (lo >= hi || (part > 0 && page < 0)) continue;
+    const Rows& in = part == 0 ? a.q : part == 1 ? a.k : a.v;
+    const T* src = static_cast<const T*>(in.data) + bs * in.batch_stride + is * in.token_stride + lo * in.head_stride;
+    T* dst;
+    long long ds;
+    if (part == 0) {
+      dst = static_cast<T*>(a.q_out.data) + bs * a.q_out.batch_stride + is * a.q_out.token_stride +
+            lo * a.q_out.head_stride;
+      ds = a.q_out.head_stride;
+    } else {
+      dst = static_cast<T*>(part == 1 ? a.k_pages : a.v_pages) + cell + (size_t)lo * kChunk * D;
+      ds = kChunk * D;
     }
-#pragma unroll
-    for (int k = 0; k < kRotHeads; ++k) {
-      const int hh = h + k;
-      if (hh < h1 && (hh < a.h || page >= 0)) {
-        T* p = target(hh);
-        if (hh < a.h + a.g) {
-          turn_unit<T, T>(r0[k], r1[k], w, p + o0, p + o1);
-        } else {
-          __stcs(reinterpret_cast<uint4*>(p + o0), r0[k]);
-          __stcs(reinterpret_cast<uint4*>(p + o1), r1[k]);
-        }
-      }
-    }
+    turn_heads<T, T>(src, in.head_stride, dst, ds, hi - lo, o0, o1, w, part == 2 ? (int)kCopied : w.how);
   }
 }
 
