@@ -822,7 +822,7 @@ def check_dense_args(shape, q, k_pages, v_pages, block_table, max_chunks, seq_le
 class DenseDecode:
     """Reusable decode call of a dense layer (every key, or a sliding window of chunks) for a
     paged cache of `max_chunks` chunks per sequence; holds the workspace, which serves one
-    call at a time (`ws`: the caller's own, zero-filled)."""
+    call at a time (`ws`: the caller's own, zero-filled before it serves another shape)."""
 
     def __init__(self, batch, heads_q, heads_kv, head_dim, max_chunks, dtype, scale=None, device="cuda", window=0,
                  ws=None):

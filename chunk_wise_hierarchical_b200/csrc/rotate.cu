@@ -164,7 +164,8 @@ __device__ __forceinline__ void turn_heads(const Tin* src, long long ss, Tout* d
 }
 
 // Heads per CTA.  One block of all heads computes the angles once but leaves 1.4 waves of CTAs
-// at the 345M prefill shape (80 us there; blocks of 16, 8 and 4 heads: 46, 44 and 48 us).
+// at the 345M prefill shape (80 us there in an earlier form, 47 us with blocks of 8; now 46 us
+// with blocks of 16 heads and 44 us with 8).
 int pick_heads(long long token_blocks, int heads) {
   int hb = heads;
   auto ctas = [&] { return token_blocks * ((heads + hb - 1) / hb); };

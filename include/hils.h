@@ -474,12 +474,18 @@ HILS_API hils_status hils_append_paged(const hils_shape* shape, const hils_rows*
  *   out          [batch, heads_q, head_dim] (dtype), written
  *   lse_out      [batch, heads_q] fp32 or NULL: log of the sum of exp(logit) over the keys
  *   ws           workspace of hils_workspace_size(HILS_OP_DECODE_DENSE) bytes, zero-filled
- *                before first use; one call at a time (calls that may run at the same time,
- *                graphs among them, take a workspace each)
+ *                before first use and before it serves another shape: the error word,
+ *                partial sums and the counters of their parts, which every call leaves at
+ *                zero.  One call at a time: calls that may run at the same time, graphs
+ *                among them, take a workspace each
+ * The result does not depend on timing: the same arguments give the same bits.
  * seq_lens[b] <= 0 gives a zero row and lse -inf, and so does a row whose every logit is
  * -inf.  What the pages hold at and after position seq_lens[b] is not looked at: it may be
- * anything, NaN included.  Page ids outside [0, n_pages) are skipped and flagged, and so are
- * the keys of a length beyond max_chunks * B.
+ * anything, NaN included.  (An infinite value before it gives NaN in bf16, where its weight
+ * is split in two.)  Page ids outside [0, n_pages) are skipped and flagged, and so are the
+ * keys of a length beyond max_chunks * B.
+ * heads_kv * max_chunks is limited to 2^29 and n_pages * heads_kv to 2^31; beyond them, and
+ * for a window above 128 chunks, the call returns HILS_ERR_UNSUPPORTED.
  */
 HILS_API hils_status hils_decode_dense(const hils_shape* shape, const void* q, const void* k_pages,
                                        const void* v_pages, const int32_t* block_table, int32_t max_chunks,

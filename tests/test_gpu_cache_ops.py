@@ -534,6 +534,29 @@ def test_dense_repeats_bit_for_bit_and_on_another_stream():
     assert torch.equal(call(**t), out)
 
 
+def test_two_graphs_that_share_a_workspace():
+    """One after the other on one stream, in any order, each keeps its own result."""
+    t, _ = _dense_case([3000, 700, 0], 8, 2, 128, "bf16", seed=20)
+    u, _ = _dense_case([900, 2800, 64], 8, 2, 128, "bf16", seed=21)
+    m = t["block_table"].shape[1]
+    u["block_table"] = torch.nn.functional.pad(u["block_table"], (0, m - u["block_table"].shape[1]), value=-1)
+    call = hils.DenseDecode(3, 8, 2, 128, m, torch.bfloat16)
+    want = [call(**x).clone() for x in (t, u)]
+    graphs, outs = [], []
+    for x in (t, u):
+        out = torch.empty_like(x["q"])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(**x, out=out)
+        graphs.append(g)
+        outs.append(out)
+    for i in (0, 1, 1, 0, 1, 0):
+        outs[i].fill_(9)
+        graphs[i].replay()
+        assert torch.equal(outs[i], want[i])
+    assert call.device_status() == 0
+
+
 def test_two_workspaces_at_once():
     t, _ = _dense_case([3000, 700], 8, 2, 64, "bf16", seed=17)
     u, _ = _dense_case([900, 2800], 8, 2, 64, "bf16", seed=18)
