@@ -747,13 +747,20 @@ class Append:
         s, dt, dev, i32 = self.shape, self.dtype, self.dev, torch.int32
         ks, ps = k.shape, k_pages.shape
         b, h, g, d = s.batch, s.heads_q, s.heads_kv, s.head_dim
-        # packed tokens as they mostly come, in one expression; any other call goes through the
-        # full check, which says what is wrong
-        if not (len(ks) == 3 and new_lens is None and ks[1] == g and ks[2] == d and k.dtype is dt and v.dtype is dt and
-                v.shape == ks and k.get_device() == dev and v.get_device() == dev and
-                k.stride(-1) == 1 and v.stride(-1) == 1 and
-                (ks[0] == b if cu_new is None else
-                 cu_new.shape == (b + 1,) and cu_new.dtype is i32 and cu_new.get_device() == dev) and
+        if len(ks) == 3:
+            n = tokens = ks[0]
+            rows, qrows, ragged, entries = (n, g, d), (n, h, d), cu_new, b + 1
+            right = new_lens is None and (cu_new is not None or n == b)
+        else:
+            n = ks[2] if len(ks) == 4 else 0
+            tokens, rows, qrows, ragged, entries = b * n, (b, g, n, d), (b, h, n, d), new_lens, b
+            right = cu_new is None
+        # what makes the call right, in one expression; where it does not hold, the full check
+        # says what is wrong
+        if not (right and ks == rows and v.shape == rows and k.dtype is dt and v.dtype is dt and
+                k.get_device() == dev and v.get_device() == dev and k.stride(-1) == 1 and v.stride(-1) == 1 and
+                (ragged is None or
+                 ragged.shape == (entries,) and ragged.dtype is i32 and ragged.get_device() == dev) and
                 len(ps) == 4 and ps[1] == g and ps[2] == 64 and ps[3] == d and v_pages.shape == ps and
                 k_pages.dtype is dt and v_pages.dtype is dt and
                 k_pages.get_device() == dev and v_pages.get_device() == dev and
@@ -761,26 +768,22 @@ class Append:
                 block_table.get_device() == dev and
                 seq_lens.shape == (b,) and seq_lens.dtype is i32 and seq_lens.get_device() == dev and
                 (q_out is None if q is None else
-                 q.shape == (ks[0], h, d) and q.dtype is dt and q.get_device() == dev and q.stride(-1) == 1 and
-                 (q_out is None or q_out.shape == q.shape and q_out.dtype is dt and q_out.get_device() == dev and
+                 q.shape == qrows and q.dtype is dt and q.get_device() == dev and q.stride(-1) == 1 and
+                 (q_out is None or q_out.shape == qrows and q_out.dtype is dt and q_out.get_device() == dev and
                   q_out.stride(-1) == 1)) and
-                (full_pages is None or full_pages.shape == (append_slots(b, ks[0]),) and full_pages.dtype is i32 and
+                (full_pages is None or full_pages.shape == (append_slots(b, tokens),) and full_pages.dtype is i32 and
                  full_pages.get_device() == dev)):
             check_append_args(s, k, v, k_pages, v_pages, block_table, self.max_chunks, seq_lens, q, q_out, cu_new,
                               new_lens, full_pages)
             _same_device(k, self.ws)
         if q is not None and q_out is None:
             q_out = _empty(q.shape, q.dtype, k, stream)
-        if len(ks) == 4:
-            n_new, rows = ks[2], _rows4
-        elif cu_new is None:  # one token per sequence: [b, heads, 1, d]
-            n_new, rows = 1, _rows_single
-        else:
-            n_new, rows = ks[0], _rows_packed
-        _launch(lib().hils_append_paged, "hils_append_paged", k, stream, s, rows(k), rows(v),
-                None if q is None else rows(q), None if q is None else rows(q_out), n_new, _at(cu_new), _at(new_lens),
-                _at(seq_lens), _at(block_table), self.max_chunks, k_pages.shape[0], self.rope, _at(k_pages),
-                _at(v_pages), _at(full_pages), _at(self.ws), self.ws.numel())
+        pack = _rows4 if len(ks) == 4 else _rows_packed if cu_new is not None else _rows_single
+        _launch(lib().hils_append_paged, "hils_append_paged", k, stream, s, pack(k), pack(v),
+                None if q is None else pack(q), None if q is None else pack(q_out),
+                1 if pack is _rows_single else n, _at(cu_new), _at(new_lens), _at(seq_lens), _at(block_table),
+                self.max_chunks, ps[0], self.rope, _at(k_pages), _at(v_pages), _at(full_pages), _at(self.ws),
+                self.ws.numel())
         return q_out
 
     def device_status(self, stream=None):

@@ -71,7 +71,7 @@ struct DenseCfg {
   static constexpr int kWeights = G * kJoinMost;
   static constexpr int kSums = kDenseThreads * 4;
   static constexpr int kQ = sizeof(T) == 4 ? G * D : 0;          // per warp: queries and weights of the fp32 path
-  static constexpr int kP = sizeof(T) == 4 ? 16 * G : 0;
+  static constexpr int kP = sizeof(T) == 4 ? (kTile + 4) * G : 0;
   static constexpr size_t kSmem = 1024 + (size_t)kRings + 4ull * (kHeads + kWeights + kSums + kDenseWarps * (kQ + kP));
   static_assert(kStages >= 1 && kTile % 16 == 0 && G * D * 4 <= kDenseRing, "a unit fills a stage, an output fits one");
   static_assert(kSmem <= 227 * 1024 - 10 * 1024, "room for the static shared variables");
@@ -274,108 +274,170 @@ struct WarpStateBf16 {
   }
 };
 
-// fp32: CUDA cores.  For the scores lane l takes keys pr and pr + 8 of the slice, pr a
+// fp32: CUDA cores.  For the scores lane l takes keys pr, pr + 8, ... of the unit, pr a
 // permutation of l / 4 that keeps the swizzled 16-byte reads free of bank conflicts, and the
-// quarter l % 4 of the head; for the output it owns D / 32 adjacent columns of every head.
+// quarter l % 4 of the head; each query read from shared memory serves all its keys.  With four
+// heads or more the quarters' sums are scattered as they are reduced: lane l ends with the
+// logits of heads l % 4, l % 4 + 4 and does the softmax of those alone.  For the output it owns
+// D / 32 adjacent columns of every head.
 template <int D, int G>
 struct WarpStateF32 {
+  static constexpr int kTile = DenseCfg<float, D, G>::kTile;
+  static constexpr int NR = kTile / 8;             // keys of a lane
+  static constexpr int NH = G >= 4 ? G / 4 : G;    // heads whose softmax it does
   static constexpr int kCpl = D / 32;
-  float m[G], l[G], o[G][kCpl];
+  float m[NH], l[NH], o[G][kCpl];
+
+  static __device__ __forceinline__ int head(int j, int lane) { return G >= 4 ? (lane & 3) + 4 * j : j; }
 
   __device__ void start(const DenseArgs& a, int bi, int gi, float* sq, int lane) {
     const float* row = static_cast<const float*>(a.q) + ((size_t)bi * a.h + gi * G) * D;
     for (int x = lane; x < G * D; x += 32) sq[x] = __ldg(row + x);
     __syncwarp();
 #pragma unroll
-    for (int hh = 0; hh < G; ++hh) {
-      m[hh] = -INFINITY;
-      l[hh] = 0.f;
+    for (int j = 0; j < NH; ++j) {
+      m[j] = -INFINITY;
+      l[j] = 0.f;
+    }
+#pragma unroll
+    for (int hh = 0; hh < G; ++hh)
 #pragma unroll
       for (int x = 0; x < kCpl; ++x) o[hh][x] = 0.f;
+  }
+
+  // The sum over the quarters of one key's logits s, of the lane's heads.
+  static __device__ __forceinline__ void reduce(const float (&s)[G], float (&x)[NH], int lane) {
+    if constexpr (G >= 4) {
+      // lanes 2 apart exchange the heads that the other keeps (bit 1 of the head), then 1 apart
+      float y[G / 2];
+#pragma unroll
+      for (int j = 0; j < G / 2; ++j) {
+        const int lo = (j >> 1) * 4 + (j & 1), hi = lo + 2;
+        const float keep = lane & 2 ? s[hi] : s[lo], send = lane & 2 ? s[lo] : s[hi];
+        y[j] = keep + __shfl_xor_sync(0xffffffffu, send, 2);
+      }
+#pragma unroll
+      for (int j = 0; j < NH; ++j) {
+        const float keep = lane & 1 ? y[2 * j + 1] : y[2 * j], send = lane & 1 ? y[2 * j] : y[2 * j + 1];
+        x[j] = keep + __shfl_xor_sync(0xffffffffu, send, 1);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NH; ++j) {
+        x[j] = s[j] + __shfl_xor_sync(0xffffffffu, s[j], 1);
+        x[j] += __shfl_xor_sync(0xffffffffu, x[j], 2);
+      }
     }
   }
 
-  // A unit with `valid` keys (> 0), 16 at a time.
+  // A unit with `valid` keys (> 0).  sp: [kTile][G] weights, then [G] factors.
   __device__ void consume(uint32_t sk, uint32_t sv, int valid, float scale, const float* sq, float* sp, int lane) {
-    for (int row0 = 0; row0 < valid; row0 += 16) slice(sk, sv, row0, valid, scale, sq, sp, lane);
-  }
-  __device__ __forceinline__ void slice(uint32_t sk, uint32_t sv, int row0, int valid, float scale, const float* sq,
-                                        float* sp, int lane) {
     constexpr uint32_t kSub = DenseCfg<float, D, G>::kSub;
     const int rr = lane >> 2, c = lane & 3;
     const int pr = ((rr & 1) << 2) | (rr >> 1);
-    float sa[G], sb[G];
+    float s[NR][G];
 #pragma unroll
-    for (int hh = 0; hh < G; ++hh) sa[hh] = sb[hh] = 0.f;
-#pragma unroll 4
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int hh = 0; hh < G; ++hh) s[r][hh] = 0.f;
+#pragma unroll 2
     for (int i = 0; i < D / 16; ++i) {
       const uint32_t base = sk + (i >> 1) * kSub, j = c + 4 * (i & 1);
-      const float4 ka = lds4(base + tc::sw128_chunk(row0 + pr, j)), kb = lds4(base + tc::sw128_chunk(row0 + 8 + pr, j));
+      float4 k[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) k[r] = lds4(base + tc::sw128_chunk(8 * r + pr, j));
 #pragma unroll
       for (int hh = 0; hh < G; ++hh) {
         const float4 q = *reinterpret_cast<const float4*>(sq + hh * D + (c + 4 * i) * 4);
-        sa[hh] = fmaf(q.x, ka.x, fmaf(q.y, ka.y, fmaf(q.z, ka.z, fmaf(q.w, ka.w, sa[hh]))));
-        sb[hh] = fmaf(q.x, kb.x, fmaf(q.y, kb.y, fmaf(q.z, kb.z, fmaf(q.w, kb.w, sb[hh]))));
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+          s[r][hh] = fmaf(q.x, k[r].x, fmaf(q.y, k[r].y, fmaf(q.z, k[r].z, fmaf(q.w, k[r].w, s[r][hh]))));
       }
     }
+    float x[NR][NH], f[NH];
 #pragma unroll
-    for (int hh = 0; hh < G; ++hh) {
+    for (int r = 0; r < NR; ++r) {
+      reduce(s[r], x[r], lane);
 #pragma unroll
-      for (int d = 1; d < 4; d <<= 1) {
-        sa[hh] += __shfl_xor_sync(0xffffffffu, sa[hh], d);
-        sb[hh] += __shfl_xor_sync(0xffffffffu, sb[hh], d);
-      }
-      const float xa = row0 + pr < valid ? sa[hh] * scale : -INFINITY;
-      const float xb = row0 + 8 + pr < valid ? sb[hh] * scale : -INFINITY;
-      float t = fmaxf(xa, xb), base;
+      for (int j = 0; j < NH; ++j) x[r][j] = 8 * r + pr < valid ? x[r][j] * scale : -INFINITY;
+    }
+    bool raised = false;
+#pragma unroll
+    for (int j = 0; j < NH; ++j) {
+      float t = x[0][j], base;
+#pragma unroll
+      for (int r = 1; r < NR; ++r) t = fmaxf(t, x[r][j]);
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
-      const float f = raise_max(m[hh], t, base);
-      const float pa = exp2f(xa - base), pb = exp2f(xb - base);
-      l[hh] = l[hh] * f + (pa + pb);
+      f[j] = raise_max(m[j], t, base);
+      raised |= f[j] != 1.f;
+      l[j] *= f[j];
 #pragma unroll
-      for (int x = 0; x < kCpl; ++x) o[hh][x] *= f;
-      if ((hh & 3) == c) {
-        sp[pr * G + hh] = pa;
-        sp[(8 + pr) * G + hh] = pb;
+      for (int r = 0; r < NR; ++r) {
+        const float p = exp2f(x[r][j] - base);
+        l[j] += p;
+        if (G >= 4 || c == j) sp[(8 * r + pr) * G + head(j, lane)] = p;
+      }
+      if (rr == 0 && (G >= 4 || c == j)) sp[kTile * G + head(j, lane)] = f[j];
+    }
+    raised = __any_sync(0xffffffffu, raised);
+    __syncwarp();
+    if (raised) {
+#pragma unroll
+      for (int hh = 0; hh < G; ++hh) {
+        const float g = sp[kTile * G + hh];
+#pragma unroll
+        for (int y = 0; y < kCpl; ++y) o[hh][y] *= g;
       }
     }
-    __syncwarp();
-    const int nk = min(16, valid - row0);  // the values behind the last key are not read
     const uint32_t piece = lane * kCpl / 4;
     const uint32_t vb = sv + (piece >> 3) * kSub + (lane * kCpl % 4) * 4;
 #pragma unroll 4
-    for (int j = 0; j < nk; ++j) {
-      const uint32_t addr = vb + tc::sw128_chunk(row0 + j, piece & 7);
-      float v[kCpl];
+    for (int j = 0; j < min(kTile, valid); ++j) {  // the values behind the last key are not read
+      const uint32_t addr = vb + tc::sw128_chunk(j, piece & 7);
+      float v[kCpl], p[G];
       if constexpr (kCpl == 4) {
-        const float4 x = lds4(addr);
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+        const float4 y = lds4(addr);
+        v[0] = y.x; v[1] = y.y; v[2] = y.z; v[3] = y.w;
       } else {
-        const float2 x = lds2(addr);
-        v[0] = x.x; v[1] = x.y;
+        const float2 y = lds2(addr);
+        v[0] = y.x; v[1] = y.y;
+      }
+      if constexpr (G >= 4) {
+#pragma unroll
+        for (int hh = 0; hh < G; hh += 4) {
+          const float4 y = *reinterpret_cast<const float4*>(sp + j * G + hh);
+          p[hh] = y.x; p[hh + 1] = y.y; p[hh + 2] = y.z; p[hh + 3] = y.w;
+        }
+      } else {
+#pragma unroll
+        for (int hh = 0; hh < G; ++hh) p[hh] = sp[j * G + hh];
       }
 #pragma unroll
-      for (int hh = 0; hh < G; ++hh) {
-        const float p = sp[j * G + hh];
+      for (int hh = 0; hh < G; ++hh)
 #pragma unroll
-        for (int x = 0; x < kCpl; ++x) o[hh][x] = fmaf(p, v[x], o[hh][x]);
-      }
+        for (int y = 0; y < kCpl; ++y) o[hh][y] = fmaf(p[hh], v[y], o[hh][y]);
     }
     __syncwarp();
   }
 
   __device__ void finish() {
 #pragma unroll
-    for (int hh = 0; hh < G; ++hh)
+    for (int j = 0; j < NH; ++j)
 #pragma unroll
-      for (int d = 4; d < 32; d <<= 1) l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], d);
+      for (int d = 4; d < 32; d <<= 1) l[j] += __shfl_xor_sync(0xffffffffu, l[j], d);
+  }
+  // m and l of head hh, from the lane that has them
+  __device__ __forceinline__ float2 of(int hh) const {
+    const int j = G >= 4 ? hh / 4 : hh, from = G >= 4 ? hh % 4 : 0;
+    return make_float2(__shfl_sync(0xffffffffu, m[j], from), __shfl_sync(0xffffffffu, l[j], from));
   }
   __device__ void write(float* out, float* lse, int lane) {
 #pragma unroll
     for (int hh = 0; hh < G; ++hh) {
-      const float inv = inverse_sum(l[hh]);
-      if (lse && lane == 0) lse[hh] = log_sum(m[hh], l[hh]);
+      const float2 ml = of(hh);
+      const float inv = inverse_sum(ml.y);
+      if (lse && lane == 0) lse[hh] = log_sum(ml.x, ml.y);
 #pragma unroll
       for (int x = 0; x < kCpl; ++x) out[hh * D + lane * kCpl + x] = o[hh][x] * inv;
     }
@@ -383,7 +445,8 @@ struct WarpStateF32 {
   __device__ void leave(float* so, float2* ml, int lane) {
 #pragma unroll
     for (int hh = 0; hh < G; ++hh) {
-      if (lane == 0) ml[hh] = make_float2(m[hh], l[hh]);
+      const float2 y = of(hh);
+      if (lane == 0) ml[hh] = y;
 #pragma unroll
       for (int x = 0; x < kCpl; ++x) so[hh * D + lane * kCpl + x] = o[hh][x];
     }
