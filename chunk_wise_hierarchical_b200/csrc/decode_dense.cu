@@ -531,6 +531,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
     s_abort = 0;
     s_prefix[0] = 0;
   }
+  wait_for_stream();
   {  // units before each sequence: thread t counts sequences 4 t .. 4 t + 3
     constexpr int kPer = kDenseSeqs / kDenseThreads;
     unsigned mine[kPer], sum = 0;
@@ -891,8 +892,7 @@ static cudaError_t launch_dense(const DenseKernelArgs& ka, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev <= 63) ready.fetch_or(bit);
   }
-  decode_dense_kernel<T, D, G><<<kDenseCtas, kDenseThreads, C::kSmem, st>>>(ka);
-  return cudaGetLastError();
+  return launch_overlapped(decode_dense_kernel<T, D, G>, kDenseCtas, kDenseThreads, C::kSmem, st, ka);
 }
 
 template <typename T, int D>

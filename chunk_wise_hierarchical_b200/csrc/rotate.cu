@@ -181,6 +181,7 @@ template <typename Tin, typename Tout, int D>
 __global__ void __launch_bounds__(kRotThreads) rotate_kernel(RotateArgs a) {
   constexpr int E = Unit<Tin>::E;
   constexpr int U = D / (2 * E);  // units per row
+  wait_for_stream();
   const int heads = a.heads[0] + a.heads[1];
   const int n_hb = (heads + a.head_block - 1) / a.head_block;
   const int h0 = (int)(blockIdx.x % n_hb) * a.head_block, h1 = min(heads, h0 + a.head_block);
@@ -215,8 +216,7 @@ static cudaError_t launch_rotate_d(RotateArgs a, cudaStream_t st) {
   a.head_block = pick_heads(token_blocks, heads);
   const long long blocks = token_blocks * ((heads + a.head_block - 1) / a.head_block);
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  rotate_kernel<Tin, Tout, D><<<(unsigned)blocks, kRotThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(rotate_kernel<Tin, Tout, D>, (unsigned)blocks, kRotThreads, 0, st, a);
 }
 template <typename Tin, typename Tout>
 static cudaError_t launch_rotate(const RotateArgs& a, cudaStream_t st) {
@@ -251,6 +251,7 @@ __global__ void __launch_bounds__(kRotThreads) append_kernel(AppendArgs a, int n
   constexpr int E = Unit<T>::E;
   constexpr int U = D / (2 * E);
   __shared__ int32_t s_cu[kRotSeqs + 1];
+  wait_for_stream();
   const int t = threadIdx.x;
   const bool packed = a.cu_new != nullptr;
   const int32_t* cu = a.cu_new;
@@ -344,8 +345,7 @@ static cudaError_t launch_append(AppendArgs a, cudaStream_t st) {
   const long long blocks = n_work + (a.n_slots + kRotThreads - 1) / kRotThreads;
   if (blocks == 0) return cudaSuccess;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  append_kernel<T, D><<<(unsigned)blocks, kRotThreads, 0, st>>>(a, (int)n_work);
-  return cudaGetLastError();
+  return launch_overlapped(append_kernel<T, D>, (unsigned)blocks, kRotThreads, 0, st, a, (int)n_work);
 }
 
 cudaError_t run_append(const AppendArgs& a, cudaStream_t st) {
