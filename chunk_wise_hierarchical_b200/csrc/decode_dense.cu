@@ -26,6 +26,14 @@
 // took about 500 cycles a unit; a 16 KB unit is 700 cycles of the SM's share of HBM), and units
 // dealt to the warps in turn, joined at the end of every (sequence, KV head) (about 2 us each,
 // which batches of short sequences do not hide).
+//
+// Measured (events around graphs of 20 calls, caches beyond L2, bf16): 8 sequences of 32K, 16
+// heads of 64, 164 us (1.07 GB, 6.6 TB/s); 33 sequences of 0 to 16K, 32 heads over 8 of 128,
+// 172 us (1.13 GB, 6.6 TB/s); one of 512K, the same heads, 313 us (2.15 GB, 6.9 TB/s); 64 of up
+// to 2K 51 us (5.4 TB/s); one of 1013 tokens 7.1 us, a chain of latencies: lengths, block
+// table, copy, one unit's products, ticket, join.  The tensor pipe is 15% busy.  fp32 with one
+// head or few per KV head reads at 6.0 to 6.6 TB/s; with eight it is bound by the CUDA cores
+// (262K of 2 KV heads: 61 us at d = 64, 4.4 TB/s, and 111 us at d = 128, 4.8 TB/s).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -45,13 +53,18 @@ constexpr int kDenseThreads = kDenseWarps * 32;
 constexpr int kDenseCtas = 148;          // one per SM
 constexpr int kDenseSeqs = 1024;         // sequences of one launch (their prefix sums in shared memory)
 constexpr int kDenseMaxTiles = 4;        // units of a chunk and KV head, at most
-constexpr int kDenseMinUnits = 4;        // units of a CTA, at least
-constexpr int kJoinMost = 32;            // partials joined in one step (one per lane)
-constexpr int kJoinBlock = 13;           // more are joined in blocks of this many first
+// Units of a CTA, at least: more SMs for a short context read it sooner and then join more parts
+// (1013 tokens, 8 KV heads of 128: 9.0 us with 2, 7.4 with 4, 9.1 with 8).
+constexpr int kDenseMinUnits = 4;
+// Partials joined in one step, one per lane; more (one KV head over up to 148 SMs) are joined in
+// blocks of kJoinBlock first, by different SMs (262K of one KV head, 8 heads of 128: 37 us with
+// all 148 parts read by one SM, 32 us so).
+constexpr int kJoinMost = 32;
+constexpr int kJoinBlock = 13;
 
-// Bytes of a warp's ring.  Eight warps have 128 KB in flight, which reaches the card's read
-// rate; 192 KB lose some of it again (one 512K context, 7B heads: 306 us with 128 KB, 317 us
-// with 192 KB), and so do smaller units.
+// Bytes of a warp's ring: one unit.  Eight warps have 128 KB in flight, which reaches the card's
+// read rate; 192 KB lose some of it again (one 512K context, 7B heads: 306 us with 128 KB, 317 us
+// with 192 KB, in the form with a producer warp), and so do two units of 8 KB (308 and 316 us).
 constexpr int kDenseRing = 16 * 1024;
 
 // T element, D head dim, G heads per KV head.

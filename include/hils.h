@@ -103,7 +103,8 @@ typedef struct {
 HILS_API const char* hils_status_string(int status);
 
 /* ABI version, currently 3 (1 had no window field and no lse_out; 2 had no
- * hils_set_wait_limit). */
+ * hils_set_wait_limit; hils_rotate, hils_append_paged and hils_decode_dense are
+ * additions to 3). */
 HILS_API int32_t hils_abi_version(void);
 
 /* Default of hils_set_wait_limit: about a second or more of polling. */
