@@ -470,8 +470,8 @@ def backward(q, k, v, landmark, out, lse, topk_idx, topk_score, dout, scale=None
 _FLOATS = (torch.bfloat16, torch.float32)
 # The device and stream that a launch finds, without the Python objects around them: these
 # calls come once per decoded token.
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 class _on:

@@ -19,7 +19,7 @@
 // pushed half-written output lines out of it (345M prefill shape: 55 -> 47 us).  Measured:
 // q and k of the 345M prefill shape, slices of a fused projection, 44 us (268 MB, 6.1 TB/s);
 // fp32 gradients of the 16K training shape 165 us (1.07 GB, 6.5 TB/s); 20K prompt tokens of the
-// 7B shape appended in 81 us (490 MB, 6.1 TB/s); one token for each of 64 sequences 3.9 us.
+// 7B shape appended in 80 us (490 MB, 6.1 TB/s); one token for each of 64 sequences 3.6 us.
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -163,9 +163,11 @@ __device__ __forceinline__ void turn_heads(const Tin* src, long long ss, Tout* d
   }
 }
 
-// Heads per CTA.  One block of all heads computes the angles once but leaves 1.4 waves of CTAs
-// at the 345M prefill shape (80 us there in an earlier form, 47 us with blocks of 8; now 46 us
-// with blocks of 16 heads and 44 us with 8).
+// Heads per CTA.  One block of all heads computes the angles once but leaves few waves of CTAs:
+// at the 345M prefill shape 80 us in an earlier form against 47 with blocks of 8; now 46 us with
+// blocks of 16 heads, 44 with 8, and with 8 waves wanted instead of 32 45 us there and 88 instead
+// of 80 for 20K prompt tokens.  Few tokens are spread further, down to one head a CTA: one token
+// for each of 64 sequences 3.6 us, 4.0 with all heads in one block.
 int pick_heads(long long token_blocks, int heads) {
   int hb = heads;
   auto ctas = [&] { return token_blocks * ((heads + hb - 1) / hb); };
