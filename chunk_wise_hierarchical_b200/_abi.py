@@ -528,9 +528,9 @@ def _dense_shape(batch, heads_q, heads_kv, head_dim, max_chunks, dtype, scale=No
                       HILS_BF16 if dtype in (torch.bfloat16, "bf16") else HILS_F32, scale=scale or 0.0, window=window)
 
 
-def _launch(fn, where, t, stream, *args):
-    """fn(*args, stream) on tensor t's device and, unless `stream` is given, its current stream."""
-    dev = t.get_device()
+def _launch(fn, args, t, dev, stream, where):
+    """fn(*args, stream) on device dev, tensor t's, and, unless `stream` is given, its current
+    stream."""
     if stream is None and dev >= 0 and _current_device() == dev:
         st = fn(*args, _raw_stream(dev))
     else:
@@ -538,16 +538,6 @@ def _launch(fn, where, t, stream, *args):
             st = fn(*args, raw)
     if st != 0:
         raise HilsError(st, where)
-
-
-def _at(t):
-    """The address of a dense tensor (0: none).  Its device has been compared with that of the
-    tensor that the call is launched on."""
-    if t is None:
-        return None
-    if not t.is_contiguous():
-        raise ValueError("tensor must be contiguous")
-    return t.data_ptr()
 
 
 def _empty(shape, dtype, t, stream):
@@ -574,19 +564,20 @@ def _rope_bytes(inv_freq, interleaved, d):
 
 def _rows4(t):
     """[b, heads, n, d] as hils_rows."""
-    st = t.stride()
-    return _pack_rows(t.data_ptr(), st[0], st[1], st[2])
+    a, b, c, e = t.stride()
+    if e != 1:
+        raise ValueError("the last dimension of q, k, v and their outputs must be contiguous")
+    return _pack_rows(t.data_ptr(), a, b, c)
 
 
-def _contiguous_rows(*ts):
-    for t in ts:
-        if t is not None and t.stride(-1) != 1:
-            raise ValueError("the last dimension of q, k, v and their outputs must be contiguous")
+def _not_contiguous():
+    raise ValueError("tensors other than the rows of q, k, v and their outputs must be contiguous")
 
 
 def check_rotate_args(q, inv_freq, k=None, positions=None, q_out=None, k_out=None):
     """The tensors of rotate against one another; returns the stride of positions over the
-    batch (0: shared).  Alignment and overlaps are checked by hils_rotate."""
+    batch (0: shared).  Strides, alignment and overlaps are checked where the rows are packed and
+    by hils_rotate."""
     if q.dim() != 4:
         raise ValueError("q must be [b, heads_q, n, d]")
     b, _, n, d = q.shape
@@ -604,7 +595,6 @@ def check_rotate_args(q, inv_freq, k=None, positions=None, q_out=None, k_out=Non
             _expect(k_out, k.shape, (q.dtype if q_out is None else q_out.dtype,), "k_out")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _contiguous_rows(q, k, q_out, k_out)
     _same_device(q, inv_freq, k, positions, q_out, k_out)
     if positions is None:
         return 0
@@ -629,43 +619,50 @@ def rotate(q, inv_freq, k=None, positions=None, inverse=False, interleaved=False
     contiguous and 16-byte aligned; an output may be its input (in place), and may be bf16 or
     fp32 whatever the input is."""
     qs, dt, dev = q.shape, q.dtype, q.get_device()
+    ks = None if k is None else k.shape
     # the call as it mostly comes, in one expression; any other goes through the full check,
     # which says what is wrong
-    if (len(qs) == 4 and dt in _FLOATS and inv_freq is not None and inv_freq.get_device() == dev and
+    if (ks is not None and len(qs) == 4 and len(ks) == 4 and dt in _FLOATS and k.dtype is dt and
+            ks[0] == qs[0] and ks[2] == qs[2] and ks[3] == qs[3] and k.get_device() == dev and
+            inv_freq is not None and inv_freq.get_device() == dev and
             (positions is None or positions.shape == (qs[0], qs[2]) and positions.dtype is torch.int32 and
-             positions.get_device() == dev and positions.is_contiguous()) and k is not None and k.dtype is dt and k.get_device() == dev and
-            k.shape[2:] == qs[2:] and k.shape[0] == qs[0] and k.stride(-1) == 1 and q.stride(-1) == 1 and
-            (q_out is None or q_out.shape == qs and q_out.dtype is dt and q_out.get_device() == dev and
-             q_out.stride(-1) == 1) and
-            (k_out is None or q_out is not None and k_out.shape == k.shape and k_out.dtype is dt and
-             k_out.get_device() == dev and k_out.stride(-1) == 1)):
+             positions.get_device() == dev and positions.is_contiguous()) and
+            (q_out is None or q_out.shape == qs and q_out.dtype is dt and q_out.get_device() == dev) and
+            (k_out is None or q_out is not None and k_out.shape == ks and k_out.dtype is dt and
+             k_out.get_device() == dev)):
         pstride = 0 if positions is None else qs[2]
     else:
         pstride = check_rotate_args(q, inv_freq, k, positions, q_out, k_out)
     b, h, n, d = qs
-    if q_out is None:
-        q_out = _empty(q.shape, q.dtype, q, stream)
-    if k is not None and k_out is None:
-        k_out = _empty(k.shape, q_out.dtype, q, stream)
     rope = _rope_bytes(inv_freq, interleaved, d)
-    g = h if k is None else k.shape[1]
+    if q_out is None:
+        q_out = _empty(qs, dt, q, stream)
+    if ks is not None and k_out is None:
+        k_out = _empty(ks, q_out.dtype, q, stream)
+    g = h if ks is None else ks[1]
     if b * n * h * g:
-        _launch(lib().hils_rotate, "hils_rotate", q, stream, _shape_of(b, h, g, d, n, 0, _dt(q)), _rows4(q),
-                None if k is None else _rows4(k), rope, None if positions is None else positions.data_ptr(), pstride,
-                1 if inverse else 0, _rows4(q_out), None if k is None else _rows4(k_out), _dt(q_out))
-    return q_out if k is None else (q_out, k_out)
+        bf16, out_bf16 = 1 if dt is torch.bfloat16 else 0, 1 if q_out.dtype is torch.bfloat16 else 0
+        _launch(lib().hils_rotate,
+                (_shape_of(b, h, g, d, n, 0, bf16), _rows4(q), None if ks is None else _rows4(k), rope,
+                 None if positions is None else positions.data_ptr(), pstride, 1 if inverse else 0, _rows4(q_out),
+                 None if ks is None else _rows4(k_out), out_bf16), q, dev, stream, "hils_rotate")
+    return q_out if ks is None else (q_out, k_out)
 
 
 def _rows_single(t):
     """[b, heads, d], one token each, as hils_rows."""
-    st = t.stride()
-    return _pack_rows(t.data_ptr(), st[0], st[1], 0)
+    a, b, e = t.stride()
+    if e != 1:
+        raise ValueError("the last dimension of q, k, v and their outputs must be contiguous")
+    return _pack_rows(t.data_ptr(), a, b, 0)
 
 
 def _rows_packed(t):
     """[tokens, heads, d] as hils_rows."""
-    st = t.stride()
-    return _pack_rows(t.data_ptr(), 0, st[1], st[0])
+    a, b, e = t.stride()
+    if e != 1:
+        raise ValueError("the last dimension of q, k, v and their outputs must be contiguous")
+    return _pack_rows(t.data_ptr(), 0, b, a)
 
 
 def append_slots(batch, tokens):
@@ -676,8 +673,8 @@ def append_slots(batch, tokens):
 
 def check_append_args(shape, k, v, k_pages, v_pages, block_table, max_chunks, seq_lens, q=None, q_out=None,
                       cu_new=None, new_lens=None, full_pages=None):
-    """The tensors of an append against the shape (see Append.__call__).  Alignment and
-    overlaps are checked by hils_append_paged."""
+    """The tensors of an append against the shape (see Append.__call__).  Strides, alignment and
+    overlaps are checked where the rows are packed and by hils_append_paged."""
     b, h, g, d = shape.batch, shape.heads_q, shape.heads_kv, shape.head_dim
     dts = (_dtype_of(shape),)
     if k.dim() == 3:
@@ -714,7 +711,6 @@ def check_append_args(shape, k, v, k_pages, v_pages, block_table, max_chunks, se
         raise ValueError("q_out without q")
     if full_pages is not None:
         _expect(full_pages, (append_slots(b, tokens),), (torch.int32,), "full_pages")
-    _contiguous_rows(k, v, q, q_out)
     _same_device(k, v, q, q_out, k_pages, v_pages, block_table, seq_lens, cu_new, new_lens, full_pages)
 
 
@@ -731,7 +727,7 @@ class Append:
         self.rope = None if inv_freq is None else _rope_bytes(inv_freq, interleaved, head_dim)
         self.ws = _own_workspace(self.shape, OP_APPEND, device, ws)
         _same_device(self.ws, inv_freq)
-        self.dev, self.dtype = self.ws.get_device(), _dtype_of(self.shape)
+        self._dims = (batch, heads_q, heads_kv, head_dim, _dtype_of(self.shape), self.ws.get_device())
 
     def __call__(self, k, v, k_pages, v_pages, block_table, seq_lens, q=None, q_out=None, cu_new=None, new_lens=None,
                  full_pages=None, stream=None):
@@ -744,9 +740,8 @@ class Append:
         seq_lens [b] int32 are the lengths after the call.  full_pages: int32
         [append_slots(b, tokens)], receives the pages filled by the call, else -1: it can go to
         summarize_paged as it is.  q_out may be q itself."""
-        s, dt, dev, i32 = self.shape, self.dtype, self.dev, torch.int32
-        ks, ps = k.shape, k_pages.shape
-        b, h, g, d = s.batch, s.heads_q, s.heads_kv, s.head_dim
+        b, h, g, d, dt, dev = self._dims
+        i32, ks, ps = torch.int32, k.shape, k_pages.shape
         if len(ks) == 3:
             n = tokens = ks[0]
             rows, qrows, ragged, entries = (n, g, d), (n, h, d), cu_new, b + 1
@@ -757,8 +752,8 @@ class Append:
             right = cu_new is None
         # what makes the call right, in one expression; where it does not hold, the full check
         # says what is wrong
-        if not (right and ks == rows and v.shape == rows and k.dtype is dt and v.dtype is dt and
-                k.get_device() == dev and v.get_device() == dev and k.stride(-1) == 1 and v.stride(-1) == 1 and
+        if not (right and ks == rows and v.shape == ks and k.dtype is dt and v.dtype is dt and
+                k.get_device() == dev and v.get_device() == dev and
                 (ragged is None or
                  ragged.shape == (entries,) and ragged.dtype is i32 and ragged.get_device() == dev) and
                 len(ps) == 4 and ps[1] == g and ps[2] == 64 and ps[3] == d and v_pages.shape == ps and
@@ -768,22 +763,27 @@ class Append:
                 block_table.get_device() == dev and
                 seq_lens.shape == (b,) and seq_lens.dtype is i32 and seq_lens.get_device() == dev and
                 (q_out is None if q is None else
-                 q.shape == qrows and q.dtype is dt and q.get_device() == dev and q.stride(-1) == 1 and
-                 (q_out is None or q_out.shape == qrows and q_out.dtype is dt and q_out.get_device() == dev and
-                  q_out.stride(-1) == 1)) and
-                (full_pages is None or full_pages.shape == (append_slots(b, tokens),) and full_pages.dtype is i32 and
+                 q.shape == qrows and q.dtype is dt and q.get_device() == dev and
+                 (q_out is None or q_out.shape == qrows and q_out.dtype is dt and q_out.get_device() == dev)) and
+                (full_pages is None or full_pages.shape == (b + tokens // 64,) and full_pages.dtype is i32 and
                  full_pages.get_device() == dev)):
-            check_append_args(s, k, v, k_pages, v_pages, block_table, self.max_chunks, seq_lens, q, q_out, cu_new,
-                              new_lens, full_pages)
+            check_append_args(self.shape, k, v, k_pages, v_pages, block_table, self.max_chunks, seq_lens, q, q_out,
+                              cu_new, new_lens, full_pages)
             _same_device(k, self.ws)
+        if not (k_pages.is_contiguous() and v_pages.is_contiguous() and block_table.is_contiguous() and
+                seq_lens.is_contiguous() and (ragged is None or ragged.is_contiguous()) and
+                (full_pages is None or full_pages.is_contiguous())):
+            _not_contiguous()
         if q is not None and q_out is None:
-            q_out = _empty(q.shape, q.dtype, k, stream)
+            q_out = _empty(q.shape, dt, k, stream)
         pack = _rows4 if len(ks) == 4 else _rows_packed if cu_new is not None else _rows_single
-        _launch(lib().hils_append_paged, "hils_append_paged", k, stream, s, pack(k), pack(v),
-                None if q is None else pack(q), None if q is None else pack(q_out),
-                1 if pack is _rows_single else n, _at(cu_new), _at(new_lens), _at(seq_lens), _at(block_table),
-                self.max_chunks, ps[0], self.rope, _at(k_pages), _at(v_pages), _at(full_pages), _at(self.ws),
-                self.ws.numel())
+        _launch(lib().hils_append_paged,
+                (self.shape, pack(k), pack(v), None if q is None else pack(q), None if q is None else pack(q_out),
+                 1 if pack is _rows_single else n, None if cu_new is None else cu_new.data_ptr(),
+                 None if new_lens is None else new_lens.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
+                 self.max_chunks, ps[0], self.rope, k_pages.data_ptr(), v_pages.data_ptr(),
+                 None if full_pages is None else full_pages.data_ptr(), self.ws.data_ptr(), self.ws.numel()),
+                k, dev, stream, "hils_append_paged")
         return q_out
 
     def device_status(self, stream=None):
@@ -832,30 +832,35 @@ class DenseDecode:
         self.max_chunks = max_chunks
         self.shape = _dense_shape(batch, heads_q, heads_kv, head_dim, max_chunks, dtype, scale, window)
         self.ws = _own_workspace(self.shape, OP_DECODE_DENSE, device, ws)
-        self.dev, self.dtype = self.ws.get_device(), _dtype_of(self.shape)
+        self._dims = (batch, heads_q, heads_kv, head_dim, _dtype_of(self.shape), self.ws.get_device())
 
     def __call__(self, q, k_pages, v_pages, block_table, seq_lens, out=None, lse=None, stream=None):
         """out [b,h,d] (q's dtype); lse, if given (fp32 [b,h]), receives log sum exp(logit)."""
-        s, dt, dev, i32 = self.shape, self.dtype, self.dev, torch.int32
-        b, qs, ps = s.batch, q.shape, k_pages.shape
-        # in one expression; where it does not hold, the full check says what is wrong
-        if not (qs == (b, s.heads_q, s.head_dim) and q.dtype is dt and q.get_device() == dev and
-                len(ps) == 4 and ps[1] == s.heads_kv and ps[2] == 64 and ps[3] == s.head_dim and
-                v_pages.shape == ps and k_pages.dtype is dt and v_pages.dtype is dt and
+        b, h, g, d, dt, dev = self._dims
+        i32, qs, ps = torch.int32, q.shape, k_pages.shape
+        # what makes the call right, in one expression; where it does not hold, the full check
+        # says what is wrong
+        if not (qs == (b, h, d) and q.dtype is dt and q.get_device() == dev and
+                len(ps) == 4 and ps[1] == g and ps[2] == 64 and ps[3] == d and v_pages.shape == ps and
+                k_pages.dtype is dt and v_pages.dtype is dt and
                 k_pages.get_device() == dev and v_pages.get_device() == dev and
                 block_table.shape == (b, self.max_chunks) and block_table.dtype is i32 and
                 block_table.get_device() == dev and
                 seq_lens.shape == (b,) and seq_lens.dtype is i32 and seq_lens.get_device() == dev and
                 (out is None or out.shape == qs and out.dtype is dt and out.get_device() == dev) and
-                (lse is None or lse.shape == (b, s.heads_q) and lse.dtype is torch.float32 and
-                 lse.get_device() == dev)):
-            check_dense_args(s, q, k_pages, v_pages, block_table, self.max_chunks, seq_lens, out, lse)
+                (lse is None or lse.shape == (b, h) and lse.dtype is torch.float32 and lse.get_device() == dev)):
+            check_dense_args(self.shape, q, k_pages, v_pages, block_table, self.max_chunks, seq_lens, out, lse)
             _same_device(q, self.ws)
         if out is None:
-            out = _empty(q.shape, q.dtype, q, stream)
-        _launch(lib().hils_decode_dense, "hils_decode_dense", q, stream, self.shape, _at(q), _at(k_pages),
-                _at(v_pages), _at(block_table), self.max_chunks, _at(seq_lens), k_pages.shape[0], _at(out), _at(lse),
-                _at(self.ws), self.ws.numel())
+            out = _empty(qs, dt, q, stream)
+        if not (q.is_contiguous() and k_pages.is_contiguous() and v_pages.is_contiguous() and
+                block_table.is_contiguous() and seq_lens.is_contiguous() and out.is_contiguous() and
+                (lse is None or lse.is_contiguous())):
+            _not_contiguous()
+        _launch(lib().hils_decode_dense,
+                (self.shape, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+                 self.max_chunks, seq_lens.data_ptr(), ps[0], out.data_ptr(), None if lse is None else lse.data_ptr(),
+                 self.ws.data_ptr(), self.ws.numel()), q, dev, stream, "hils_decode_dense")
         return out
 
     def device_status(self, stream=None):

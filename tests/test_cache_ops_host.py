@@ -102,7 +102,6 @@ def test_rotate_arguments():
     dict(positions=torch.zeros(2 * N, dtype=torch.int32)[::2]),
     dict(q_out=torch.zeros(B, H, N, D, dtype=torch.float16)),
     dict(q_out=torch.zeros(B, H, N + 1, D, dtype=BF)),
-    dict(q_out=torch.zeros(B, H, D, N, dtype=BF).transpose(2, 3)),
     dict(k_out=torch.zeros(B, G, N, D, dtype=BF)),
     dict(inv_freq=None),
 ])
@@ -169,12 +168,27 @@ def test_structs_are_packed_as_declared():
     assert (o.inv_freq, o.rotary_dim, o.interleaved) == (f.data_ptr(), 48, 1)
 
 
-def test_rows_need_contiguous_last_dimension():
-    x = torch.zeros(2, 3, 64, 8, dtype=BF).transpose(2, 3)
-    with pytest.raises(ValueError):
-        check_rotate_args(x, torch.ones(16))
-    with pytest.raises(ValueError):
-        check_rotate_args(torch.zeros(2, 3, 8, 64, dtype=BF), torch.ones(16), q_out=x)
+def test_tensors_that_are_not_contiguous_are_refused():
+    x = torch.zeros(2, 3, 64, 8, dtype=BF).transpose(2, 3)  # rows of stride 8
+    y = torch.zeros(2, 3, 8, 64, dtype=BF)
+    _refused(hils.rotate, x, torch.ones(16))
+    _refused(hils.rotate, y, torch.ones(16), q_out=x)
+    _refused(hils.rotate, y, torch.ones(16), k=x)
+    call = hils.Append(B, H, G, D, 3, BF, ws=_ws())
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    for kw in (dict(k=torch.zeros(9, D, G, dtype=BF).transpose(1, 2)), dict(q=torch.zeros(9, D, H, dtype=BF).transpose(1, 2)),
+               dict(k_pages=torch.zeros(5, 64, G, D, dtype=BF).transpose(1, 2)), dict(block_table=i(3, B).T),
+               dict(seq_lens=i(2 * B)[::2]), dict(cu_new=i(2 * B + 2)[::2]), dict(full_pages=i(2 * B)[::2])):
+        a = _append_args(**kw)
+        a.pop("max_chunks")
+        _refused(call, **a)
+    call = hils.DenseDecode(B, H, G, D, 3, BF, ws=_ws())
+    for kw in (dict(q=torch.zeros(B, D, H, dtype=BF).transpose(1, 2)), dict(lse=torch.zeros(H, B).T),
+               dict(out=torch.zeros(H, B, D, dtype=BF).transpose(0, 1)), dict(block_table=i(3, B).T),
+               dict(v_pages=torch.zeros(5, 64, G, D, dtype=BF).transpose(1, 2)), dict(seq_lens=i(2 * B)[::2])):
+        a = _dense_args(**kw)
+        a.pop("max_chunks")
+        _refused(call, **a)
 
 
 def _append_args(dtype=BF, **kw):
