@@ -30,10 +30,10 @@
 // Measured (events around graphs of 20 calls, caches beyond L2, bf16): 8 sequences of 32K, 16
 // heads of 64, 164 us (1.07 GB, 6.6 TB/s); 33 sequences of 0 to 16K, 32 heads over 8 of 128,
 // 172 us (1.13 GB, 6.6 TB/s); one of 512K, the same heads, 313 us (2.15 GB, 6.9 TB/s); 64 of up
-// to 2K 51 us (5.4 TB/s); one of 1013 tokens 7.1 us, a chain of latencies: lengths, block
+// to 2K 51 us (5.4 TB/s); one of 1013 tokens 6.9 us, a chain of latencies: lengths, block
 // table, copy, one unit's products, ticket, join.  The tensor pipe is 15% busy.  fp32 with one
-// head or few per KV head reads at 6.0 to 6.6 TB/s; with eight it is bound by the CUDA cores
-// (262K of 2 KV heads: 61 us at d = 64, 4.4 TB/s, and 111 us at d = 128, 4.8 TB/s).
+// head or few per KV head reads at 6.1 to 6.6 TB/s; with eight it is bound by the CUDA cores
+// (262K of 2 KV heads: 60 us at d = 64, 4.5 TB/s, and 110 us at d = 128, 4.9 TB/s).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -511,6 +511,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
   extern __shared__ unsigned char smem_raw[];
   __shared__ unsigned s_prefix[kDenseSeqs + 1];  // units before each sequence
   __shared__ int s_len[kDenseSeqs];
+  __shared__ unsigned s_own_prefix[kDenseWarps][33];  // the same of at most 32 sequences, one copy a warp
+  __shared__ int s_own_len[kDenseWarps][32];
   __shared__ __align__(16) unsigned s_scan[kDenseWarps];
   __shared__ uint64_t s_full[kDenseWarps][C::kStages];
   __shared__ Segment s_seg[2 * kDenseWarps];     // the segment in each warp slot (nt 0: none)
@@ -542,31 +544,47 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
     asm volatile("prefetch.tensormap [%0];" ::"l"(&ka.tmap_k) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&ka.tmap_v) : "memory");
     s_abort = 0;
-    s_prefix[0] = 0;
   }
   wait_for_stream();
-  {  // units before each sequence: thread t counts sequences 4 t .. 4 t + 3
+  // ---- units before each sequence
+  const unsigned* prefix = s_prefix;
+  const int* len = s_len;
+  const long long cap = (long long)a.max_chunks * kChunk;
+  auto length_of = [&](int b) {
+    int L = b < a.b ? a.seq_lens[b] : 0;
+    if (L > cap) {
+      if (blockIdx.x == 0) set_error(a.err, kErrBadPage);
+      L = (int)cap;
+    }
+    return L;
+  };
+  auto up_to = [&](unsigned x) {  // inclusive sum over the lanes
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    return x;
+  };
+  if (a.b <= 32) {  // each warp for itself, without barriers (7 sequences, window of 512: 9.0 -> 8.5 us a call)
+    const int L = length_of(lane);
+    s_own_len[warp][lane] = L;
+    s_own_prefix[warp][lane + 1] = up_to((unsigned)n_tiles<C::kTile>(L, a.n_win) * (unsigned)a.g);
+    if (lane == 0) s_own_prefix[warp][0] = 0;
+    prefix = s_own_prefix[warp];
+    len = s_own_len[warp];
+    __syncwarp();
+  } else {  // thread t counts sequences 4 t .. 4 t + 3
     constexpr int kPer = kDenseSeqs / kDenseThreads;
     unsigned mine[kPer], sum = 0;
-    const long long cap = (long long)a.max_chunks * kChunk;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int b = t * kPer + i;
-      int L = b < a.b ? a.seq_lens[b] : 0;
-      if (L > cap) {
-        if (blockIdx.x == 0) set_error(a.err, kErrBadPage);
-        L = (int)cap;
-      }
-      s_len[b] = L;
+      const int L = length_of(t * kPer + i);
+      s_len[t * kPer + i] = L;
       sum += (unsigned)n_tiles<C::kTile>(L, a.n_win) * (unsigned)a.g;
       mine[i] = sum;
     }
-    unsigned inc = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const unsigned y = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += y;
-    }
+    const unsigned inc = up_to(sum);
     if (lane == 31) s_scan[warp] = inc;
     sum = inc - sum;  // before this thread, within the warp
     __syncthreads();
@@ -574,9 +592,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
     for (int w = 0; w < kDenseWarps; ++w) sum += w < warp ? s_scan[w] : 0u;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) s_prefix[t * kPer + i + 1] = sum + mine[i];
+    if (t == 0) s_prefix[0] = 0;
+    __syncthreads();
   }
-  __syncthreads();
-  const unsigned total = s_prefix[a.b];
+  const unsigned total = prefix[a.b];
   const unsigned per = max((unsigned)kDenseMinUnits, (total + kDenseCtas - 1) / kDenseCtas);
   const unsigned u0 = min(total, blockIdx.x * per), u1 = min(total, u0 + per);
   const unsigned per_warp = (u1 - u0 + kDenseWarps - 1) / kDenseWarps;
@@ -584,9 +603,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
   auto segment_of = [&](int b, unsigned u) {  // the segment of unit u of sequence b
     Segment g;
     g.bi = b;
-    g.nt = n_tiles<C::kTile>(s_len[b], a.n_win);
-    g.gi = (int)(u - s_prefix[b]) / g.nt;
-    g.lo = s_prefix[b] + (unsigned)g.gi * g.nt;
+    g.nt = n_tiles<C::kTile>(len[b], a.n_win);
+    g.gi = (int)(u - prefix[b]) / g.nt;
+    g.lo = prefix[b] + (unsigned)g.gi * g.nt;
     g.hi = g.lo + g.nt;
     return g;
   };
@@ -599,9 +618,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
     z = -1;
     y = 0;
     if (u >= w1) return;
-    const int b = seq_of(s_prefix, a.b, u);
+    const int b = seq_of(prefix, a.b, u);
     const Segment g = segment_of(b, u);
-    const int tile = first_tile<C::kTile>(s_len[b], a.n_win) + (int)(u - g.lo);
+    const int tile = first_tile<C::kTile>(len[b], a.n_win) + (int)(u - g.lo);
     const int page = a.block_table[(size_t)b * a.max_chunks + tile * C::kTile / kChunk];
     y = tile * C::kTile % kChunk;
     if (page >= 0 && page < a.n_pages) z = page * a.g + g.gi;
@@ -635,15 +654,16 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
     ++issued;
   };
   while (issued < mine && issued < (unsigned)C::kStages) issue();
+  __syncthreads();  // s_abort is clear
   unsigned phases = 0;  // bit s: parity of the next fill of stage s to wait for
 
   if (t == 0) {  // for the end, while the first units are on their way
     s_cut[0].nt = s_cut[1].nt = 0;
     if (u0 < u1) {
-      const Segment first = segment_of(seq_of(s_prefix, a.b, u0), u0);
+      const Segment first = segment_of(seq_of(prefix, a.b, u0), u0);
       if (first.lo < u0 || first.hi > u1) s_cut[0] = first;
       if (first.hi < u1) {
-        const Segment last = segment_of(seq_of(s_prefix, a.b, u1 - 1), u1 - 1);
+        const Segment last = segment_of(seq_of(prefix, a.b, u1 - 1), u1 - 1);
         if (last.hi > u1) s_cut[1] = last;
       }
     }
@@ -651,7 +671,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
 
   // sequences without keys
   for (int b = blockIdx.x; b < a.b; b += kDenseCtas) {
-    if (s_len[b] > 0) continue;
+    if (len[b] > 0) continue;
     for (int x = t; x < a.h * D / 4; x += kDenseThreads)
       store4(out + (size_t)b * a.h * D + x * 4, make_float4(0.f, 0.f, 0.f, 0.f));
     if (a.lse)
@@ -660,13 +680,13 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
 
   const float scale = a.scale * 1.4426950408889634f;  // logits in units of log 2
   bool failed = false;
-  int bi = w0 < w1 ? seq_of(s_prefix, a.b, w0) : 0;
+  int bi = w0 < w1 ? seq_of(prefix, a.b, w0) : 0;
   unsigned u = w0;
   while (u < w1) {
-    while (s_prefix[bi + 1] <= u) ++bi;
+    while (prefix[bi + 1] <= u) ++bi;
     const Segment g = segment_of(bi, u);
     const unsigned ue = min(w1, g.hi);
-    const int first = first_tile<C::kTile>(s_len[bi], a.n_win);
+    const int first = first_tile<C::kTile>(len[bi], a.n_win);
     WarpState<T, D, G> w;
     w.start(a, bi, g.gi, s_q, lane);
     for (; u < ue; ++u) {
@@ -677,7 +697,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
         if (failed) break;
         phases ^= 1u << st;
         const uint32_t sk = ring + st * C::kStage;
-        w.consume(sk, sk + C::kHalf, min(C::kTile, s_len[bi] - (first + (int)(u - g.lo)) * C::kTile), scale, s_q, s_p,
+        w.consume(sk, sk + C::kHalf, min(C::kTile, len[bi] - (first + (int)(u - g.lo)) * C::kTile), scale, s_q, s_p,
                   lane);
         __syncwarp();
       }
