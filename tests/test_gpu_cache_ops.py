@@ -252,6 +252,10 @@ def test_append_of_many_sequences():
     counts = [int(rng.randint(1, 80)) if i % 7 == 0 else 0 for i in range(700)]
     lens = [c + int(rng.randint(0, 70)) for c in counts]
     assert _append_check("packed", counts, lens, 1, 1, 64, "bf16", 64, False) == 0
+    # more than the kernel keeps the offsets of in shared memory
+    counts = [int(rng.randint(1, 9)) if i % 5 == 0 else 0 for i in range(1500)]
+    lens = [c + int(rng.randint(0, 70)) for c in counts]
+    assert _append_check("packed", counts, lens, 1, 1, 64, "f32", 32, True) == 0
 
 
 def test_append_skips_and_flags_bad_pages():
@@ -445,6 +449,39 @@ def test_dense_batches_of_short_sequences(b, h, g, d, most, window):
         t, _ = _dense_case(lens, h, g, d, dtype, seed=b, needles=False)
         out, lse = _dense_run(t, window=window)
         _dense_close_gpu(out, lse, t, lens, window)
+
+
+def test_dense_with_tables_far_wider_than_the_lengths():
+    """Tables of 67M tokens a sequence: one launch counts the units of 63 of them in 32 bits."""
+    b, h, g, d = 70, 8, 8, 64
+    t, w = _dense_case([int(x) for x in np.random.RandomState(1).randint(0, 200, b)], h, g, d, "bf16", seed=30)
+    wide = torch.full((b, 1 << 20), -1, dtype=torch.int32, device="cuda")
+    wide[:, :t["block_table"].shape[1]] = t["block_table"]
+    out, lse = _dense_run(t)
+    o, l = _dense_run({**t, "block_table": wide})
+    _dense_close_gpu(o, l, t, t["seq_lens"].tolist())
+    _dense_close_gpu(out, lse, t, t["seq_lens"].tolist())
+
+
+def test_calls_on_a_given_stream_with_a_callers_workspace():
+    t, w = _dense_case([700, 90], 4, 2, 64, "bf16", seed=31)
+    want = _dense_run(t)[0]
+    m = t["block_table"].shape[1]
+    from chunk_wise_hierarchical_b200._abi import make_shape, workspace_size
+    n = workspace_size(make_shape(2, 4, 2, 64, m * 64, 0, 1), hils.OP_DECODE_DENSE)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    call = hils.DenseDecode(2, 4, 2, 64, m, torch.bfloat16, ws=ws)
+    q4 = _randn(2, 4, 70, 64, dtype=torch.bfloat16, seed=32)
+    turned = hils.rotate(q4, _freq(64))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        out = call(**t, stream=side)
+        r = hils.rotate(q4, _freq(64), stream=side)
+        assert call.device_status(stream=side) == 0  # waits for the stream
+        assert torch.equal(out, want) and torch.equal(r, turned)
+    with pytest.raises(hils.HilsError):  # a workspace off its alignment is refused
+        hils.DenseDecode(2, 4, 2, 64, m, torch.bfloat16, ws=torch.zeros(n + 8, dtype=torch.uint8, device="cuda")[8:])(**t)
 
 
 def test_dense_every_length_of_a_ragged_batch():
