@@ -504,6 +504,11 @@ struct Segment {
   int bi, gi, nt;      // nt: its units
   unsigned lo, hi;     // [lo, hi)
 };
+// A segment that is cut between CTAs: its parts, the first of them that of CTA `first`.
+struct Cut {
+  Segment g;
+  int first, n;        // n 0: there is none
+};
 
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __grid_constant__ DenseKernelArgs ka) {
@@ -516,7 +521,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
   __shared__ __align__(16) unsigned s_scan[kDenseWarps];
   __shared__ uint64_t s_full[kDenseWarps][C::kStages];
   __shared__ Segment s_seg[2 * kDenseWarps];     // the segment in each warp slot (nt 0: none)
-  __shared__ Segment s_cut[2];                   // the segments of u0 and u1 - 1, where they are cut (nt 0: not)
+  __shared__ Cut s_cut[2];                       // the segments of u0 and u1 - 1, where they are cut
   __shared__ float2 s_ml[2 * kDenseWarps][G];
   __shared__ float s_M[G], s_z[G];
   __shared__ int s_abort, s_last[2];
@@ -658,13 +663,17 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
   unsigned phases = 0;  // bit s: parity of the next fill of stage s to wait for
 
   if (t == 0) {  // for the end, while the first units are on their way
-    s_cut[0].nt = s_cut[1].nt = 0;
+    s_cut[0].n = s_cut[1].n = 0;
+    auto note = [&](int side, const Segment& g) {
+      const int first = (int)(g.lo / per);
+      s_cut[side] = Cut{g, first, (int)((g.hi - 1) / per) - first + 1};
+    };
     if (u0 < u1) {
       const Segment first = segment_of(seq_of(prefix, a.b, u0), u0);
-      if (first.lo < u0 || first.hi > u1) s_cut[0] = first;
+      if (first.lo < u0 || first.hi > u1) note(0, first);
       if (first.hi < u1) {
         const Segment last = segment_of(seq_of(prefix, a.b, u1 - 1), u1 - 1);
-        if (last.hi > u1) s_cut[1] = last;
+        if (last.hi > u1) note(1, last);
       }
     }
   }
@@ -783,7 +792,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
   auto join = [&](int first, int j0, int step, int n) {
     auto slot = [&](int j) { return (size_t)(2 * (first + j0 + j * step) + (j0 + j * step == 0 ? 1 : 0)); };
     auto part_at = [&](int j) { return __ldcg(reinterpret_cast<const float4*>(ka.part + slot(j) * G * D) + v); };
-    constexpr int kFirst = 4;  // parts on their way while the weights are computed
+    constexpr int kFirst = 8;  // parts on their way while the weights are computed
     float4 x[kFirst];
 #pragma unroll
     for (int i = 0; i < kFirst; ++i)
@@ -832,39 +841,33 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
     asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(n - 1) : "memory");
     return old == (unsigned)(n - 1);
   };
-  // a cut segment's parts are joined at once, or in blocks first
-  auto parts_of = [&](const Segment& g, int& first) {
-    first = (int)(g.lo / per);
-    return (int)((g.hi - 1) / per) - first + 1;
+  // parts are joined at once, or in blocks first: the CTA's block, its slot and its parts
+  auto block_of = [&](const Cut& c, size_t& slot, int& j0) {
+    j0 = ((int)blockIdx.x - c.first) / kJoinBlock * kJoinBlock;
+    slot = 2 * (c.first + j0) + (j0 == 0 ? 1 : 0);
+    return min(kJoinBlock, c.n - j0);
   };
-  auto block_of = [&](int first, int n, size_t& slot, int& j0) {  // the CTA's block: its parts
-    j0 = ((int)blockIdx.x - first) / kJoinBlock * kJoinBlock;
-    slot = 2 * (first + j0) + (j0 == 0 ? 1 : 0);
-    return min(kJoinBlock, n - j0);
-  };
-  if (lane == 0 && warp < 2 && s_cut[warp].nt) {  // both tickets at once
-    const Segment g = s_cut[warp];
-    int first, j0;
-    size_t slot;
-    const int n = parts_of(g, first);
-    if (n <= kJoinMost) {
-      s_last[warp] = take(ka.ticket + (size_t)g.bi * a.g + g.gi, n);
+  if (lane == 0 && warp < 2 && s_cut[warp].n) {  // both tickets at once
+    const Cut c = s_cut[warp];
+    if (c.n <= kJoinMost) {
+      s_last[warp] = take(ka.ticket + (size_t)c.g.bi * a.g + c.g.gi, c.n);
     } else {
-      const int members = block_of(first, n, slot, j0);
+      size_t slot;
+      int j0;
+      const int members = block_of(c, slot, j0);
       s_last[warp] = take(ka.block_ticket + slot, members);
     }
   }
   __syncthreads();
   for (int side = 0; side < 2; ++side) {
-    const Segment g = s_cut[side];
-    if (g.nt == 0 || !s_last[side]) continue;
-    int first, j0 = 0, step = 1;
-    const int n = parts_of(g, first);
-    int count = n;
-    if (n > kJoinMost) {
+    const Cut c = s_cut[side];
+    if (c.n == 0 || !s_last[side]) continue;
+    int step = 1, count = c.n;
+    if (c.n > kJoinMost) {
       size_t slot;
-      const int members = block_of(first, n, slot, j0);
-      const float4 acc = join(first, j0, 1, members);
+      int j0;
+      const int members = block_of(c, slot, j0);
+      const float4 acc = join(c.first, j0, 1, members);
       // the block's sum takes the place of its first part, which has been read
       if (t < C::kVec) {
         __stcg(reinterpret_cast<float4*>(ka.part + slot * G * D) + v, acc);
@@ -872,13 +875,13 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
       }
       __syncthreads();
       step = kJoinBlock;
-      count = (n + kJoinBlock - 1) / kJoinBlock;
-      if (t == 0) s_last[side] = take(ka.ticket + (size_t)g.bi * a.g + g.gi, count);
+      count = (c.n + kJoinBlock - 1) / kJoinBlock;
+      if (t == 0) s_last[side] = take(ka.ticket + (size_t)c.g.bi * a.g + c.g.gi, count);
       __syncthreads();
       if (!s_last[side]) continue;
     }
-    const float4 acc = join(first, 0, step, count);
-    if (t < C::kVec && !s_abort) write_row(g.bi, g.gi, v, acc, s_M[hv], s_z[hv]);
+    const float4 acc = join(c.first, 0, step, count);
+    if (t < C::kVec && !s_abort) write_row(c.g.bi, c.g.gi, v, acc, s_M[hv], s_z[hv]);
     __syncthreads();
   }
 }
