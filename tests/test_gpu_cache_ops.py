@@ -103,6 +103,18 @@ def test_rotate_copies_what_lies_behind_the_rotated_part(inter):
         assert torch.isfinite(y[..., :32]).all()
 
 
+def test_rotate_beyond_32_bit_offsets():
+    """Rows whose element offsets pass 2^31, in place, at positions of their own index."""
+    n, d = (1 << 24) + 5, 128
+    x = torch.empty(1, 1, n, d, dtype=torch.bfloat16, device="cuda")
+    tail = _randn(1, 1, 9, d, dtype=torch.bfloat16, seed=50)
+    x[:, :, -9:] = tail
+    f = _freq(d)
+    hils.rotate(x, f, q_out=x)
+    want = CO.rotate(_np(tail), _np(f), list(range(n - 9, n)))
+    _close(x[:, :, -9:], want, _rotate_bound(_np(tail), want, torch.bfloat16, d, False), "rotate")
+
+
 def test_rotate_in_place_and_alone():
     q = _randn(2, 4, 130, 64, dtype=torch.bfloat16, seed=0)
     f = _freq(64)
@@ -592,6 +604,48 @@ def test_two_graphs_that_share_a_workspace():
         graphs[i].replay()
         assert torch.equal(outs[i], want[i])
     assert call.device_status() == 0
+
+
+def test_captured_after_copies_and_a_join_of_streams():
+    """The calls in a graph behind a copy, a memset and a join of two streams, each of which they
+    have to wait for."""
+    t, _ = _dense_case([2000, 700, 0], 8, 2, 64, "bf16", seed=22)
+    call = hils.DenseDecode(3, 8, 2, 64, t["block_table"].shape[1], torch.bfloat16)
+    f = _freq(64)
+    src = [_randn(3, 8, 1, 64, dtype=torch.bfloat16, seed=s) for s in (40, 41, 42)]
+    x, y = torch.empty_like(src[0]), torch.empty_like(src[0])
+    pos = torch.tensor([[1999], [699], [0]], dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    q, out, once = torch.empty_like(t["q"]), torch.empty_like(t["q"]), None
+    big = torch.randn(1 << 24, device="cuda")
+
+    def step():
+        x.copy_(y)                                        # a copy
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            z = (big * 2).sin_().sum() * 0                # long enough to be overtaken
+            pos.add_(z.int())
+        main.wait_stream(side)
+        hils.rotate(x, f, positions=pos, q_out=q.view(3, 8, 1, 64))   # behind the join
+        call(**{**t, "q": q}, out=out)
+        return hils.decode_dense(**{**t, "q": out})       # its own workspace, cleared in the graph
+
+    y.copy_(src[0])
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        once = step()
+    for s in src[1:] + src[:1]:
+        y.copy_(s)
+        graph.replay()
+        torch.cuda.synchronize()
+        qs = hils.rotate(s, f, positions=pos)
+        assert torch.equal(q, qs[:, :, 0])
+        first = _dense_run({**t, "q": q})[0]
+        assert torch.equal(out, first)
+        assert torch.equal(once, _dense_run({**t, "q": out})[0])
 
 
 def test_two_workspaces_at_once():
