@@ -112,8 +112,8 @@ HILS_API int32_t hils_abi_version(void);
 
 /*
  * hils_set_wait_limit -- sets how many times an ordinary bounded wait of the
- * tensor-core kernels (select, prefill attention) polls its mbarrier before the
- * kernel gives up.  A kernel that gives up sets the timeout bit of the error
+ * tensor-core kernels (select, prefill attention) and of the dense decode polls
+ * its mbarrier before the kernel gives up.  A kernel that gives up sets the timeout bit of the error
  * word (hils_device_status then returns HILS_ERR_DEVICE_TIMEOUT), stops issuing
  * work, waits for the copies and MMAs it has already issued (those drain waits
  * always use HILS_DEFAULT_WAIT_LIMIT), releases its tensor memory and returns
