@@ -147,9 +147,27 @@ __device__ __forceinline__ float log_sum(float m, float z) {
   return z == 0.f ? -INFINITY : (m + log2f(z)) * 0.69314718055994531f;
 }
 
-// bf16: the warp's state.  Lane l holds heads 2 (l % 4), + 1, as the columns of the transposed score tile S^T = K Q^T and of O^T = V^T P^T.  P is split into
-// bf16 hi + lo parts (two products), so that its rounding (2^-17) stays below that of the
-// output; the tensor cores have the room at this byte rate.
+// A weight p >= 0 as three bf16 parts, cut and not rounded: the leading 8 bits, the 8 after
+// them, the rest.  Together they are p (to 2^-24, see below), and each is positive where p is, so
+// that an infinite value times p is that infinity and not NaN: a part without bits of its own
+// takes p 2^-25 instead of 0.
+__device__ __forceinline__ float cut_bf16(float p) { return __uint_as_float(__float_as_uint(p) & 0xffff0000u); }
+__device__ __forceinline__ void split3(float p, float& hi, float& mid, float& lo) {
+  const float t = p * 0x1p-25f;
+  hi = cut_bf16(p);
+  const float r = fmaxf(p - hi, t);
+  mid = cut_bf16(r);
+  lo = fmaxf(r - mid, t);
+}
+// The upper halves of two floats as a pair of bf16.
+__device__ __forceinline__ uint32_t upper_halves(float lo, float hi) {
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+
+// bf16: the warp's state.  Lane l holds heads 2 (l % 4), + 1, as the columns of the transposed
+// score tile S^T = K Q^T and of O^T = V^T P^T.  P enters as three bf16 parts (three products),
+// which hold its fp32 value; two would leave 2^-17.  The tensor cores have the room at this byte
+// rate.
 template <int D, int G>
 struct WarpStateBf16 {
   static constexpr int NS = DenseCfg<__nv_bfloat16, D, G>::kTile / 16;  // 16-key products of a unit
@@ -213,8 +231,8 @@ struct WarpStateBf16 {
         o[k][0] *= c0; o[k][1] *= c1; o[k][2] *= c0; o[k][3] *= c1;
       }
     }
-    // P^T as the second operand: bf16 hi and lo parts of keys (0-7, 8-15) of each slice
-    uint32_t ph[NS][2], pl[NS][2], keep[NS][2];
+    // P^T as the second operand: the parts of keys (0-7, 8-15) of each slice
+    uint32_t ph[NS][2], pm[NS][2], pl[NS][2], keep[NS][2];
 #pragma unroll
     for (int i = 0; i < NS; ++i)
 #pragma unroll
@@ -222,9 +240,12 @@ struct WarpStateBf16 {
         const float p0 = exp2f(s[i][2 * e] - b0), p1 = exp2f(s[i][2 * e + 1] - b1);
         l[0] += p0;
         l[1] += p1;
-        const uint32_t h = tc::pack_bf16x2(p0, p1);
-        ph[i][e] = transpose8(h);
-        pl[i][e] = transpose8(tc::pack_bf16x2(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u)));
+        float h0, h1, m0, m1, l0, l1;
+        split3(p0, h0, m0, l0);
+        split3(p1, h1, m1, l1);
+        ph[i][e] = transpose8(upper_halves(h0, h1));
+        pm[i][e] = transpose8(upper_halves(m0, m1));
+        pl[i][e] = transpose8(upper_halves(l0, l1));
         // values behind the last key may be anything: they are cleared, not only weighted by 0
         const int k0 = 16 * i + 8 * e + (lane & 3) * 2;
         keep[i][e] = (k0 < valid ? 0xffffu : 0u) | (k0 + 1 < valid ? 0xffff0000u : 0u);
@@ -241,6 +262,7 @@ struct WarpStateBf16 {
           f[0] &= keep[i][0]; f[1] &= keep[i][0]; f[2] &= keep[i][1]; f[3] &= keep[i][1];
         }
         mma16816(o[k], f, ph[i][0], ph[i][1]);
+        mma16816(o[k], f, pm[i][0], pm[i][1]);
         mma16816(o[k], f, pl[i][0], pl[i][1]);
       }
     }

@@ -482,9 +482,9 @@ HILS_API hils_status hils_append_paged(const hils_shape* shape, const hils_rows*
  * The result does not depend on timing: the same arguments give the same bits.
  * seq_lens[b] <= 0 gives a zero row and lse -inf, and so does a row whose every logit is
  * -inf.  What the pages hold at and after position seq_lens[b] is not looked at: it may be
- * anything, NaN included.  (An infinite value before it gives NaN in bf16, where its weight
- * is split in two.)  Page ids outside [0, n_pages) are skipped and flagged, and so are the
- * keys of a length beyond max_chunks * B.
+ * anything, NaN included.  An infinite value before it gives that infinity where its weight
+ * is above 2^-100 of the largest, NaN where its weight is zero.  Page ids outside [0, n_pages)
+ * are skipped and flagged, and so are the keys of a length beyond max_chunks * B.
  * heads_kv * max_chunks is limited to 2^29 and n_pages * heads_kv to 2^31; beyond them, and
  * for a window above 128 chunks, the call returns HILS_ERR_UNSUPPORTED.
  */

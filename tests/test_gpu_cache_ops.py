@@ -769,3 +769,74 @@ def test_prompt_through_the_framework():
     assert (sparse.float() - out[:, :, -1].float()).abs().max() < 2e-2
     dense, dl = hils.decode_dense(last, kp, vp, table, lens, return_lse=True)
     _dense_close(dense, dl, dict(q=last, k_pages=kp, v_pages=vp, block_table=table, seq_lens=lens), 0, None)
+
+
+# ---- weights and values of the dense decode ---------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("h,g,d", [(1, 1, 64), (4, 1, 128), (8, 1, 64)])
+def test_dense_weights_keep_32_bits(dtype, h, g, d):
+    """Values that cancel: what is left shows how exactly the weights entered.  Each query has one
+    element, so a logit is one exact product times a scale of two roundings: |s log2 e| <= 2 gives
+    3 * 2^-23 absolute, exp2f 2 steps of 2^-23: a weight is off by 2^-21, and so is their sum; fp32
+    sums of 6 terms in three parts by 18 * 2^-24.  r = 2^-19 of sum p |v| holds all of them; two
+    bf16 parts (2^-17 each) do not fit."""
+    b, n = 48, 6
+    dt = DT[dtype]
+    rng = np.random.RandomState(d + h)
+    logit = torch.from_numpy(rng.uniform(0, 1.3, (b, n))).to(dt)
+    q = torch.zeros(b, h, d, dtype=dt)
+    q[:, :, 5] = 1
+    kp, vp = torch.zeros(b, g, 64, d, dtype=dt), torch.zeros(b, g, 64, d, dtype=dt)
+    kp[:, 0, :n, 5] = logit
+    p = np.exp(_np(logit))
+    p /= p.sum(-1, keepdims=True)
+    v = np.zeros((b, n, d))
+    v[:, 0] = _np(torch.from_numpy(rng.uniform(1, 2, (b, d))).to(dt))
+    for j in range(1, n):
+        left = (p[:, :j, None] * v[:, :j]).sum(1)
+        v[:, j] = _np(torch.from_numpy(-left / p[:, j, None]).to(dt))
+    vp[:, 0, :n] = torch.from_numpy(v).to(dt)
+    t = dict(q=q.cuda(), k_pages=kp.cuda(), v_pages=vp.cuda(),
+             block_table=torch.arange(b, dtype=torch.int32, device="cuda").view(b, 1),
+             seq_lens=torch.full((b,), n, dtype=torch.int32, device="cuda"))
+    out, _ = _dense_run(t, scale=1.0)
+    want = (p[..., None] * v).sum(1)[:, None].repeat(h, 1)
+    mag = (p[..., None] * np.abs(v)).sum(1)[:, None].repeat(h, 1)
+    assert np.abs(want).max() < 2.0 ** -20
+    _close(out, want, 2.0 ** -19 * mag + _u(dt) * (np.abs(want) + 2.0 ** -19 * mag), "out")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("h,g,d", [(2, 2, 64), (16, 2, 128)])
+def test_dense_infinite_values(dtype, h, g, d):
+    """A value times its weight, as the formula has it: an infinity wherever the weight is not
+    zero, NaN where both infinities meet or one meets a weight of zero; other columns are as they
+    were."""
+    lens = [200, 90, 1, 3000, 70]
+    t, w = _dense_case(lens, h, g, d, dtype, seed=60, needles=False)
+    vp, kp, bt = t["v_pages"], t["k_pages"], t["block_table"].cpu().numpy()
+    clean = {k: v.clone() for k, v in t.items()}
+    put = lambda bi, j, col, x: vp[bt[bi, j // 64], :, j % 64].__setitem__((slice(None), col), x)
+    for j in range(0, 200, 7):
+        put(0, j, j % d, math.inf)
+    put(1, 3, 9, -math.inf)
+    put(1, 80, 9, math.inf)
+    put(1, 81, 10, math.inf)
+    put(2, 0, 4, -math.inf)         # a weight of one
+    put(3, 1777, 11, -math.inf)     # in a partial
+    kp[bt[4, 0], :, 20] = -math.inf * torch.sign(t["q"][4, :: h // g]).to(kp.dtype)  # head 0 of each group: no weight
+    put(4, 20, 12, math.inf)
+    out, lse = _dense_run(t)
+    want, wlse, mag, size = _dense_want(clean, *w)
+    spot = np.zeros(want.shape)
+    for j in range(0, 200, 7):
+        spot[0, :, j % d] = math.inf
+    spot[1, :, 9], spot[1, :, 10], spot[2, :, 4], spot[3, :, 11] = math.nan, math.inf, -math.inf, -math.inf
+    got = _np(out)
+    assert np.isnan(got[4, ::h // g, 12]).all()
+    some = spot != 0
+    assert np.array_equal(got[some], spot[some], equal_nan=True)
+    rest = ~some
+    rest[4] = False
+    r = (2 * d * 2.0 ** -23 * size + 2.0 ** -16 + 3000 * 2.0 ** -23)[..., None] * mag
+    assert (np.abs(got - want)[rest] <= (r + _u(out.dtype) * (np.abs(want) + r))[rest]).all()
