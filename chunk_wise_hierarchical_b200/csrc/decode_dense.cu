@@ -166,8 +166,10 @@ __device__ __forceinline__ uint32_t upper_halves(float lo, float hi) {
 
 // bf16: the warp's state.  Lane l holds heads 2 (l % 4), + 1, as the columns of the transposed
 // score tile S^T = K Q^T and of O^T = V^T P^T.  P enters as three bf16 parts (three products),
-// which hold its fp32 value; two would leave 2^-17.  The tensor cores have the room at this byte
-// rate.
+// which hold its fp32 value; two would leave 2^-17.  A unit's products are summed by the tensor
+// core, the small parts first, and added to the running sums with a rounding: the tensor core
+// cuts its sums off, and a warp's whole run in one accumulator lost up to 2^-16.  The tensor cores
+// have the room at this byte rate.
 template <int D, int G>
 struct WarpStateBf16 {
   static constexpr int NS = DenseCfg<__nv_bfloat16, D, G>::kTile / 16;  // 16-key products of a unit
@@ -225,12 +227,6 @@ struct WarpStateBf16 {
     const float c0 = raise_max(m[0], t0, b0), c1 = raise_max(m[1], t1, b1);
     l[0] *= c0;
     l[1] *= c1;
-    if (__any_sync(0xffffffffu, c0 != 1.f || c1 != 1.f)) {
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        o[k][0] *= c0; o[k][1] *= c1; o[k][2] *= c0; o[k][3] *= c1;
-      }
-    }
     // P^T as the second operand: the parts of keys (0-7, 8-15) of each slice
     uint32_t ph[NS][2], pm[NS][2], pl[NS][2], keep[NS][2];
 #pragma unroll
@@ -254,17 +250,25 @@ struct WarpStateBf16 {
     const uint32_t vrow = (lane & 7) + ((lane >> 4) << 3), vch = (lane >> 3) & 1;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
+      uint32_t f[NS][4];
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        uint32_t f[4];
-        ldsm4_t(sv + (k >> 2) * kSub + tc::sw128_chunk(vrow + 16 * i, (k & 3) * 2 + vch), f);
+        ldsm4_t(sv + (k >> 2) * kSub + tc::sw128_chunk(vrow + 16 * i, (k & 3) * 2 + vch), f[i]);
         if (tail) {
-          f[0] &= keep[i][0]; f[1] &= keep[i][0]; f[2] &= keep[i][1]; f[3] &= keep[i][1];
+          f[i][0] &= keep[i][0]; f[i][1] &= keep[i][0]; f[i][2] &= keep[i][1]; f[i][3] &= keep[i][1];
         }
-        mma16816(o[k], f, ph[i][0], ph[i][1]);
-        mma16816(o[k], f, pm[i][0], pm[i][1]);
-        mma16816(o[k], f, pl[i][0], pl[i][1]);
       }
+#pragma unroll
+      for (int i = 0; i < NS; ++i) mma16816(t, f[i], pl[i][0], pl[i][1]);
+#pragma unroll
+      for (int i = 0; i < NS; ++i) mma16816(t, f[i], pm[i][0], pm[i][1]);
+#pragma unroll
+      for (int i = 0; i < NS; ++i) mma16816(t, f[i], ph[i][0], ph[i][1]);
+      o[k][0] = fmaf(o[k][0], c0, t[0]);
+      o[k][1] = fmaf(o[k][1], c1, t[1]);
+      o[k][2] = fmaf(o[k][2], c0, t[2]);
+      o[k][3] = fmaf(o[k][3], c1, t[3]);
     }
   }
 

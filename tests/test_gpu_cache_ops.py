@@ -840,3 +840,23 @@ def test_dense_infinite_values(dtype, h, g, d):
     rest[4] = False
     r = (2 * d * 2.0 ** -23 * size + 2.0 ** -16 + 3000 * 2.0 ** -23)[..., None] * mag
     assert (np.abs(got - want)[rest] <= (r + _u(out.dtype) * (np.abs(want) + r))[rest]).all()
+
+
+def test_dense_sums_of_a_long_run_are_rounded():
+    """Values 1 and then -1 at the same keys: every weight is cancelled by its own likeness, and
+    what is left is the error of the sums alone.  148 * 8 (sequence, KV head)s of 64 units: a
+    warp's run is one of them.  A rounded sum of u units, at most half of M = sum p |v| on its
+    way, is off by u 2^-25 M; a unit's own sum (four products of the leading parts, each cut off
+    at 2^-23; the small parts' add less than one more) by 5 * 2^-23 of its share: 42 * 2^-24 M
+    in all.  Cutting the running sum off at each of its 512 products loses about 92 * 2^-24 M."""
+    b, g, d, n = 148, 8, 64, 64
+    dt = torch.bfloat16
+    q = _randn(b, g, d, dtype=dt, seed=70)
+    half = _randn(n // 2, g, 64, d, dtype=dt, seed=71)
+    kp = torch.cat((half, half))
+    vp = torch.ones_like(kp)
+    vp[n // 2:] = -1
+    t = dict(q=q, k_pages=kp, v_pages=vp, seq_lens=torch.full((b,), 64 * n, dtype=torch.int32, device="cuda"),
+             block_table=torch.arange(n, dtype=torch.int32, device="cuda").repeat(b, 1))
+    out, _ = _dense_run(t)
+    assert out.float().abs().max() <= 42 * 2.0 ** -24 * (1 + 2.0 ** -8)
