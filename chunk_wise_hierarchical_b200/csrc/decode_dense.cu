@@ -164,30 +164,41 @@ __device__ __forceinline__ uint32_t upper_halves(float lo, float hi) {
   return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
 
-// bf16: the warp's state.  Lane l holds heads 2 (l % 4), + 1, as the columns of the transposed
-// score tile S^T = K Q^T and of O^T = V^T P^T.  P enters as three bf16 parts (three products),
-// which hold its fp32 value; two would leave 2^-17.  A unit's products are summed by the tensor
-// core, the small parts first, and added to the running sums with a rounding: the tensor core
-// cuts its sums off, and a warp's whole run in one accumulator lost up to 2^-16.  The tensor cores
-// have the room at this byte rate.
+// bf16: the warp's state.  Lane l holds columns 2 (l % 4), + 1 of the transposed score tile
+// S^T = K Q^T and of O^T = V^T P^T.  Column n belongs to head n % G.  P enters as three bf16 parts,
+// which hold its fp32 value; two would leave 2^-17.  Where a tile has columns to spare (G < 8) they
+// take the other parts of the same heads: one product with G = 1 or 2, two with 4, three with 8
+// (three products for each: 2.4% slower over twelve shapes; so 0.0%).  A
+// unit's products are summed by the tensor core, the small parts first, and added to the running
+// sums with a rounding: the tensor core cuts its sums off, and a warp's whole run in one
+// accumulator lost up to 2^-16.
 template <int D, int G>
 struct WarpStateBf16 {
   static constexpr int NS = DenseCfg<__nv_bfloat16, D, G>::kTile / 16;  // 16-key products of a unit
+  static constexpr int kProducts = G == 8 ? 3 : G == 4 ? 2 : 1;        // products of a slice with its values
   float m[2], l[2], o[D / 16][4];
   uint32_t q[D / 16][2];
 
   __device__ void start(const DenseArgs& a, int bi, int gi, float*, int lane) {
-    const int hh = lane >> 2;
     const uint32_t* row = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                            ((size_t)bi * a.h + gi * G + hh) * D);
+                                                            ((size_t)bi * a.h + gi * G + (lane >> 2) % G) * D);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      q[k][0] = hh < G ? __ldg(row + k * 8 + (lane & 3)) : 0u;
-      q[k][1] = hh < G ? __ldg(row + k * 8 + 4 + (lane & 3)) : 0u;
+      q[k][0] = __ldg(row + k * 8 + (lane & 3));
+      q[k][1] = __ldg(row + k * 8 + 4 + (lane & 3));
       o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
     }
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
+  }
+
+  // What column 2 (lane % 4) + e takes of a weight's parts in product j.  A column that is over
+  // shares the low part with another, so that no column holds a zero (see split3).
+  static __device__ __forceinline__ float part_of(int j, int e, int lane, float hi, float mid, float lo) {
+    if constexpr (G == 8) return j == 0 ? lo : j == 1 ? mid : hi;
+    else if constexpr (G == 4) return j == 0 ? 0.5f * lo : lane & 2 ? mid : hi;
+    else if constexpr (G == 2) return (lane & 3) == 0 ? hi : (lane & 3) == 1 ? mid : 0.5f * lo;
+    else return lane & 3 ? 0.5f * lo : e ? mid : hi;
   }
 
   // A unit with `valid` keys (> 0): NS 16-key products side by side, one step of the running
@@ -206,7 +217,7 @@ struct WarpStateBf16 {
         mma16816(s[i], f, q[k][0], q[k][1]);
       }
     }
-    // s[i]: keys r, r (heads 2c, 2c + 1), r + 8, r + 8, r = 16 i + lane / 4
+    // s[i]: keys r, r (columns 2c, 2c + 1), r + 8, r + 8, r = 16 i + lane / 4
     float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NS; ++i)
@@ -228,7 +239,7 @@ struct WarpStateBf16 {
     l[0] *= c0;
     l[1] *= c1;
     // P^T as the second operand: the parts of keys (0-7, 8-15) of each slice
-    uint32_t ph[NS][2], pm[NS][2], pl[NS][2], keep[NS][2];
+    uint32_t pt[kProducts][NS][2], keep[NS][2];
 #pragma unroll
     for (int i = 0; i < NS; ++i)
 #pragma unroll
@@ -239,9 +250,9 @@ struct WarpStateBf16 {
         float h0, h1, m0, m1, l0, l1;
         split3(p0, h0, m0, l0);
         split3(p1, h1, m1, l1);
-        ph[i][e] = transpose8(upper_halves(h0, h1));
-        pm[i][e] = transpose8(upper_halves(m0, m1));
-        pl[i][e] = transpose8(upper_halves(l0, l1));
+#pragma unroll
+        for (int j = 0; j < kProducts; ++j)
+          pt[j][i][e] = transpose8(upper_halves(part_of(j, 0, lane, h0, m0, l0), part_of(j, 1, lane, h1, m1, l1)));
         // values behind the last key may be anything: they are cleared, not only weighted by 0
         const int k0 = 16 * i + 8 * e + (lane & 3) * 2;
         keep[i][e] = (k0 < valid ? 0xffffu : 0u) | (k0 + 1 < valid ? 0xffff0000u : 0u);
@@ -260,11 +271,9 @@ struct WarpStateBf16 {
         }
       }
 #pragma unroll
-      for (int i = 0; i < NS; ++i) mma16816(t, f[i], pl[i][0], pl[i][1]);
+      for (int j = 0; j < kProducts; ++j)
 #pragma unroll
-      for (int i = 0; i < NS; ++i) mma16816(t, f[i], pm[i][0], pm[i][1]);
-#pragma unroll
-      for (int i = 0; i < NS; ++i) mma16816(t, f[i], ph[i][0], ph[i][1]);
+        for (int i = 0; i < NS; ++i) mma16816(t, f[i], pt[j][i][0], pt[j][i][1]);
       o[k][0] = fmaf(o[k][0], c0, t[0]);
       o[k][1] = fmaf(o[k][1], c1, t[1]);
       o[k][2] = fmaf(o[k][2], c0, t[2]);
@@ -272,12 +281,25 @@ struct WarpStateBf16 {
     }
   }
 
-  // The sums over all of the warp's keys (the lanes hold shares of l until here).
+  // The sums over all of the warp's keys and of the parts (the lanes hold shares of l, the columns
+  // those of the outputs until here).  Column h < G then holds head h.
   __device__ void finish() {
 #pragma unroll
     for (int d = 4; d < 32; d <<= 1) {
       l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
       l[1] += __shfl_xor_sync(0xffffffffu, l[1], d);
+    }
+    if constexpr (G < 8) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (G == 1 && (x & 1)) continue;
+          float y = G == 1 ? o[k][x] + o[k][x + 1] : o[k][x];  // G = 1: columns 0 to 3, of lanes 0 and 1 of four
+          if (G <= 2) y += __shfl_xor_sync(0xffffffffu, y, 1);
+          if (G >= 2) y += __shfl_xor_sync(0xffffffffu, y, 2);
+          o[k][x] = y;
+        }
     }
   }
   // The result: rows out [G][D], lse [G] (or nullptr).
