@@ -168,7 +168,7 @@ __device__ __forceinline__ uint32_t upper_halves(float lo, float hi) {
 // S^T = K Q^T and of O^T = V^T P^T.  Column n belongs to head n % G.  P enters as three bf16 parts,
 // which hold its fp32 value; two would leave 2^-17.  Where a tile has columns to spare (G < 8) they
 // take the other parts of the same heads: one product with G = 1 or 2, two with 4, three with 8
-// (three products for each: 2.4% slower over twelve shapes; so 0.0%).  A
+// (over twelve shapes 1.5% slower than two rounded parts; with three products for each 2.4%).  A
 // unit's products are summed by the tensor core, the small parts first, and added to the running
 // sums with a rounding: the tensor core cuts its sums off, and a warp's whole run in one
 // accumulator lost up to 2^-16.
