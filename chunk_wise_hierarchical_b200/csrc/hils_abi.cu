@@ -2,6 +2,7 @@
 // Every entry point checks its arguments on the host, then enqueues kernels on
 // the caller's stream; nothing here allocates device memory or synchronises
 // (except hils_device_status).
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <atomic>
@@ -203,8 +204,9 @@ cudaError_t run_prefill_attention(const hils_shape* s, const void* q, const void
 hils_status check_rows(const hils_rows* r, long long nb, long long nh, long long nt, size_t elem) {
   if (!r || !r->data || !aligned16(r->data)) return HILS_ERR_INVALID_ARG;
   const long long n[3] = {nb, nh, nt}, st[3] = {r->batch_stride, r->head_stride, r->token_stride};
-  for (int i = 0; i < 3; ++i)
-    if (n[i] > 1 && (st[i] < 0 || st[i] * (long long)elem % 16 != 0)) return HILS_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i)  // (and no stride beyond an address space, so that the sums below fit)
+    if (n[i] > 1 && (st[i] < 0 || st[i] > (1ll << 56) / (long long)elem / (n[i] - 1) || st[i] * (long long)elem % 16 != 0))
+      return HILS_ERR_INVALID_ARG;
   return HILS_OK;
 }
 // Bytes [lo, hi) that rows of (nb, nh, nt) x d elements lie in.
@@ -217,6 +219,56 @@ Span span_of(const hils_rows* r, long long nb, long long nh, long long nt, int d
   return {p, p + (size_t)((nb - 1) * r->batch_stride + (nh - 1) * r->head_stride + (nt - 1) * r->token_stride + d) * elem};
 }
 bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+// Rows as sharing() compares them: strides and row length in bytes.
+struct RowSet {
+  long long data, n[3], stride[3], row;
+};
+RowSet row_set(const hils_rows* r, long long nb, long long nh, long long nt, int d, size_t elem) {
+  const long long e = (long long)elem;
+  return {(long long)reinterpret_cast<uintptr_t>(r->data), {nb, nh, nt},
+          {r->batch_stride * e, r->head_stride * e, r->token_stride * e}, d * e};
+}
+// Whether some row of a and some row of b share a byte.  A dimension that both step by the same
+// stride moves their distance by whole strides: those are searched, the widest first, and only
+// the few steps that can bring the rows together (three where the strides nest).  One that they
+// step by different strides is taken as filled.  So slices of one fused tensor are told apart
+// exactly; other sets whose spans meet may be taken to share where they only interleave.
+bool sharing(const RowSet& a, const RowSet& b) {
+  long long end_a = a.row, end_b = b.row;  // rows meet at distances in (-end_b, end_a)
+  struct Dim {
+    long long s, lo, hi;
+  } dim[3];
+  int nd = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (a.n[i] == 0 || b.n[i] == 0) return false;
+    const long long s = a.n[i] == 1 ? b.stride[i] : a.stride[i];
+    if (a.n[i] > 1 && b.n[i] > 1 && a.stride[i] != b.stride[i]) {
+      end_a += (a.n[i] - 1) * a.stride[i];
+      end_b += (b.n[i] - 1) * b.stride[i];
+    } else if ((a.n[i] > 1 || b.n[i] > 1) && s > 0) {
+      dim[nd++] = {s, -(a.n[i] - 1), b.n[i] - 1};
+    }
+  }
+  for (int i = 0; i < nd; ++i)
+    for (int j = i + 1; j < nd; ++j)
+      if (dim[j].s > dim[i].s) std::swap(dim[i], dim[j]);
+  int steps = 0;
+  auto floor_div = [](long long x, long long y) { return x / y - (x % y < 0); };
+  auto meet = [&](auto& self, int i, long long off) -> bool {
+    if (i == nd) return -end_b < off && off < end_a;
+    long long lo = 0, hi = 0;  // what the dimensions behind this one can add
+    for (int j = i + 1; j < nd; ++j) {
+      lo += dim[j].lo * dim[j].s;
+      hi += dim[j].hi * dim[j].s;
+    }
+    const long long x0 = std::max(dim[i].lo, floor_div(-end_b - off - hi, dim[i].s) + 1);
+    const long long x1 = std::min(dim[i].hi, -floor_div(-(end_a - off - lo), dim[i].s) - 1);
+    for (long long x = x0; x <= x1; ++x)
+      if (++steps > 100 || self(self, i + 1, off + x * dim[i].s)) return true;
+    return false;
+  };
+  return meet(meet, 0, b.data - a.data);
+}
 // Whether no two rows of a written tensor share an element: by ascending stride, each
 // dimension steps over all that the dimensions below it cover.
 bool rows_apart(const hils_rows* r, long long nb, long long nh, long long nt, int d) {
@@ -543,10 +595,14 @@ hils_status hils_rotate(const hils_shape* s, const hils_rows* q, const hils_rows
     if (!rows_apart(q_out, nb, s->heads_q, nt, s->head_dim) ||
         (k && !rows_apart(k_out, nb, s->heads_kv, nt, s->head_dim)))
       return HILS_ERR_INVALID_ARG;
-    // slices of one fused tensor interleave: in place, q_out may lie between k's rows
     if ((!q_same && (overlap(qo, qi) || overlap(qo, ki))) || (!k_same && (overlap(ko, ki) || overlap(ko, qi))) ||
         (!(q_same && k_same) && overlap(qo, ko)))
       return HILS_ERR_INVALID_ARG;
+    if (k) {  // in place, slices of one fused tensor interleave: each output apart from the other tensor's rows
+      const RowSet rqo = row_set(q_out, nb, s->heads_q, nt, s->head_dim, eo), rki = row_set(k, nb, s->heads_kv, nt, s->head_dim, ei);
+      const RowSet rko = row_set(k_out, nb, s->heads_kv, nt, s->head_dim, eo), rqi = row_set(q, nb, s->heads_q, nt, s->head_dim, ei);
+      if (sharing(rqo, rki) || sharing(rko, rqi) || sharing(rqo, rko)) return HILS_ERR_INVALID_ARG;
+    }
   }
   hils::RotateArgs a{};
   a.in[0] = rows_of(q); a.out[0] = rows_of(q_out); a.heads[0] = s->heads_q;

@@ -368,3 +368,34 @@ def test_dense_rejects_before_launch():
     assert call(ws=None) == 3 and call(wsb=size - 1) == 3 and call(ws=P_((1 << 20) + 8)) == 3
     assert call(s=_sh(heads_q=6)) == 2 and call(s=_sh(window=100)) == 1
     assert call(s=_sh(batch=0)) == 0
+
+
+# ---- rows that share memory -------------------------------------------------
+def _rotate_status(q, k, qo, ko, h, g, n, b=2, d=64, dtype=1, out_dtype=1):
+    """hils_rotate's status for rows at addresses that are never read: refused before the launch
+    (1), or brought to a launch that finds no GPU (4)."""
+    if torch.cuda.is_available():
+        pytest.skip("an accepted call would be launched on the addresses")
+    ref = lambda x: None if x is None else ctypes.byref(x)
+    return hils.lib().hils_rotate(ref(_sh(batch=b, heads_q=h, heads_kv=g, head_dim=d, seq_len=n, dtype=dtype)), ref(q),
+                                  ref(k), ref(Rope(1 << 20, 32, 0)), None, 0, 0, ref(qo), ref(ko), out_dtype, None)
+
+
+def test_rotate_in_place_refuses_another_tensor_on_the_same_rows():
+    """The header's promise: in place, the other tensor may lie between the rows, not on them."""
+    n, base, far = 70, 1 << 20, 1 << 30
+    dense = lambda p, h: Rows(p, h * n * 64, n * 64, 64)
+    fused = lambda p, H: Rows(p, n * H * 64, 64, H * 64)  # a slice of [b, n, H, d]
+    ok = lambda *a, **kw: _rotate_status(*a, n=n, **kw)
+    q = dense(base, 2)
+    assert ok(q, dense(base, 2), q, dense(far, 2), 2, 2) == 1               # k is q's memory
+    assert ok(q, dense(base + 128, 2), q, dense(far, 2), 2, 2) == 1         # a row further on
+    assert ok(q, q, q, q, 2, 2) == 1                                        # all four
+    assert ok(dense(far, 2), dense(base, 2), dense(base, 2), dense(base, 2), 2, 2) == 1  # q_out on k in place
+    assert ok(dense(base, 2), dense(far, 2), dense(far + (1 << 26), 2), dense(base + 64, 2), 2, 2) == 1
+    # slices of one fused tensor, both in place
+    f = lambda i: fused(base + i * 128, 12)
+    assert ok(f(0), f(8), f(0), f(8), 8, 2) == 4                            # the model's own layout
+    assert ok(f(0), f(7), f(0), f(7), 8, 2) == 1                            # a head too early
+    assert ok(f(0), f(11), f(0), f(11), 8, 2) == 1                          # its second head is the next token's first
+    assert ok(f(0), fused(base + 8 * 128, 11), f(0), fused(base + 8 * 128, 11), 8, 2) == 1  # of another width
