@@ -653,6 +653,10 @@ hils_status hils_append_paged(const hils_shape* s, const hils_rows* k, const hil
       if (overlap(qo, kp) || overlap(qo, vp) || overlap(qi, kp) || overlap(qi, vp) ||
           (!in_place(q_out, q, nb, s->heads_q, n_new) && (overlap(qo, qi) || overlap(qo, ki) || overlap(qo, vi))))
         return HILS_ERR_INVALID_ARG;
+      const RowSet rqo = row_set(q_out, nb, s->heads_q, n_new, s->head_dim, es);
+      if (sharing(rqo, row_set(k, nb, s->heads_kv, n_new, s->head_dim, es)) ||
+          sharing(rqo, row_set(v, nb, s->heads_kv, n_new, s->head_dim, es)))
+        return HILS_ERR_INVALID_ARG;
     }
   } else if (!full_pages) {
     return HILS_OK;

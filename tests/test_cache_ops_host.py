@@ -399,3 +399,27 @@ def test_rotate_in_place_refuses_another_tensor_on_the_same_rows():
     assert ok(f(0), f(7), f(0), f(7), 8, 2) == 1                            # a head too early
     assert ok(f(0), f(11), f(0), f(11), 8, 2) == 1                          # its second head is the next token's first
     assert ok(f(0), fused(base + 8 * 128, 11), f(0), fused(base + 8 * 128, 11), 8, 2) == 1  # of another width
+
+
+def _append_status(q, qo, k, v, h, g, n, cu=FAKE):
+    """hils_append_paged's status without a workspace, which is looked at last (3: nothing else
+    is wrong)."""
+    ref = ctypes.byref
+    return hils.lib().hils_append_paged(ref(_sh(heads_q=h, heads_kv=g)), ref(k), ref(v), ref(q), ref(qo), n, cu, None, FAKE,
+                                        FAKE, 4, 4, None, P_(5 << 28), P_(6 << 28), None, None, 256, None)
+
+
+def test_append_in_place_refuses_keys_and_values_on_the_queries_rows():
+    base, far = 1 << 20, 1 << 26
+    f = lambda i, H=12: Rows(base + i * 128, 0, 64, H * 64)  # packed slices of [tokens, H, d]
+    for cu in (FAKE, None):  # packed; one row per sequence and head
+        r = f if cu else lambda i, H=12: Rows(base + i * 128, H * 64, 64, 0)
+        n = 9 if cu else 1
+        assert _append_status(r(0), r(0), r(8), r(10), 8, 2, n, cu) == 3
+        assert _append_status(r(0), r(0), r(7), r(10), 8, 2, n, cu) == 1
+        assert _append_status(r(0), r(0), r(8), r(0), 8, 2, n, cu) == 1
+        assert _append_status(r(0), r(0), r(8), r(11), 8, 2, n, cu) == 1   # the next token's queries
+        assert _append_status(r(0), r(0), Rows(far, 192, 64, 192), r(10), 8, 2, n, cu) == 3
+    padded = lambda p, h, n: Rows(p, h * n * 64, n * 64, 64)
+    assert _append_status(padded(base, 4, 9), padded(base, 4, 9), padded(base, 2, 9), padded(far, 2, 9), 4, 2, 9, None) == 1
+    assert _append_status(padded(base, 4, 9), padded(base, 4, 9), padded(far, 2, 9), padded(2 * far, 2, 9), 4, 2, 9, None) == 3
