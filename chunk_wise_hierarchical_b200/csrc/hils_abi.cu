@@ -585,23 +585,16 @@ hils_status hils_rotate(const hils_shape* s, const hils_rows* q, const hils_rows
     if (k && ((st = check_rows(k, nb, s->heads_kv, nt, ei)) != HILS_OK ||
               (st = check_rows(k_out, nb, s->heads_kv, nt, eo)) != HILS_OK))
       return st;
-    // each output apart from every other tensor, its own input in place excepted
-    const Span none{0, 0};
-    const Span qi = span_of(q, nb, s->heads_q, nt, s->head_dim, ei), qo = span_of(q_out, nb, s->heads_q, nt, s->head_dim, eo);
-    const Span ki = k ? span_of(k, nb, s->heads_kv, nt, s->head_dim, ei) : none;
-    const Span ko = k ? span_of(k_out, nb, s->heads_kv, nt, s->head_dim, eo) : none;
-    const bool q_same = ei == eo && in_place(q_out, q, nb, s->heads_q, nt);
-    const bool k_same = k && ei == eo && in_place(k_out, k, nb, s->heads_kv, nt);
     if (!rows_apart(q_out, nb, s->heads_q, nt, s->head_dim) ||
         (k && !rows_apart(k_out, nb, s->heads_kv, nt, s->head_dim)))
       return HILS_ERR_INVALID_ARG;
-    if ((!q_same && (overlap(qo, qi) || overlap(qo, ki))) || (!k_same && (overlap(ko, ki) || overlap(ko, qi))) ||
-        (!(q_same && k_same) && overlap(qo, ko)))
-      return HILS_ERR_INVALID_ARG;
-    if (k) {  // in place, slices of one fused tensor interleave: each output apart from the other tensor's rows
-      const RowSet rqo = row_set(q_out, nb, s->heads_q, nt, s->head_dim, eo), rki = row_set(k, nb, s->heads_kv, nt, s->head_dim, ei);
-      const RowSet rko = row_set(k_out, nb, s->heads_kv, nt, s->head_dim, eo), rqi = row_set(q, nb, s->heads_q, nt, s->head_dim, ei);
-      if (sharing(rqo, rki) || sharing(rko, rqi) || sharing(rqo, rko)) return HILS_ERR_INVALID_ARG;
+    // each output apart from every other tensor, its own input in place excepted
+    const RowSet qi = row_set(q, nb, s->heads_q, nt, s->head_dim, ei), qo = row_set(q_out, nb, s->heads_q, nt, s->head_dim, eo);
+    if (!(ei == eo && in_place(q_out, q, nb, s->heads_q, nt)) && sharing(qo, qi)) return HILS_ERR_INVALID_ARG;
+    if (k) {
+      const RowSet ki = row_set(k, nb, s->heads_kv, nt, s->head_dim, ei), ko = row_set(k_out, nb, s->heads_kv, nt, s->head_dim, eo);
+      if (!(ei == eo && in_place(k_out, k, nb, s->heads_kv, nt)) && sharing(ko, ki)) return HILS_ERR_INVALID_ARG;
+      if (sharing(qo, ki) || sharing(ko, qi) || sharing(qo, ko)) return HILS_ERR_INVALID_ARG;
     }
   }
   hils::RotateArgs a{};
@@ -650,12 +643,11 @@ hils_status hils_append_paged(const hils_shape* s, const hils_rows* k, const hil
       const Span qi = span_of(q, nb, s->heads_q, n_new, s->head_dim, es);
       const Span qo = span_of(q_out, nb, s->heads_q, n_new, s->head_dim, es);
       if (!rows_apart(q_out, nb, s->heads_q, n_new, s->head_dim)) return HILS_ERR_INVALID_ARG;
-      if (overlap(qo, kp) || overlap(qo, vp) || overlap(qi, kp) || overlap(qi, vp) ||
-          (!in_place(q_out, q, nb, s->heads_q, n_new) && (overlap(qo, qi) || overlap(qo, ki) || overlap(qo, vi))))
-        return HILS_ERR_INVALID_ARG;
-      const RowSet rqo = row_set(q_out, nb, s->heads_q, n_new, s->head_dim, es);
-      if (sharing(rqo, row_set(k, nb, s->heads_kv, n_new, s->head_dim, es)) ||
-          sharing(rqo, row_set(v, nb, s->heads_kv, n_new, s->head_dim, es)))
+      if (overlap(qo, kp) || overlap(qo, vp) || overlap(qi, kp) || overlap(qi, vp)) return HILS_ERR_INVALID_ARG;
+      const RowSet rows = row_set(q_out, nb, s->heads_q, n_new, s->head_dim, es);
+      if ((!in_place(q_out, q, nb, s->heads_q, n_new) && sharing(rows, row_set(q, nb, s->heads_q, n_new, s->head_dim, es))) ||
+          sharing(rows, row_set(k, nb, s->heads_kv, n_new, s->head_dim, es)) ||
+          sharing(rows, row_set(v, nb, s->heads_kv, n_new, s->head_dim, es)))
         return HILS_ERR_INVALID_ARG;
     }
   } else if (!full_pages) {

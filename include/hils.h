@@ -415,8 +415,10 @@ typedef struct {
  *   positions    NULL: token i is at position i; else int32 [seq_len], or
  *                [batch, seq_len] with position_stride = seq_len (0: shared by the batch)
  *   out_dtype    hils_dtype of q_out and k_out
- * An output may be its input's own memory (same data, strides and type; the other tensor may
- * then lie between its rows, as slices of one fused tensor do); any other overlap is refused.
+ * An output may be its input's own memory (same data, strides and type).  Rows of two tensors
+ * may lie between one another, as slices of one fused tensor do; an output that shares an element
+ * with another tensor of rows is refused, and so are rows that interleave with strides of
+ * different size.
  */
 HILS_API hils_status hils_rotate(const hils_shape* shape, const hils_rows* q, const hils_rows* k,
                                  const hils_rope* rope, const int32_t* positions, int64_t position_stride,

@@ -423,3 +423,61 @@ def test_append_in_place_refuses_keys_and_values_on_the_queries_rows():
     padded = lambda p, h, n: Rows(p, h * n * 64, n * 64, 64)
     assert _append_status(padded(base, 4, 9), padded(base, 4, 9), padded(base, 2, 9), padded(far, 2, 9), 4, 2, 9, None) == 1
     assert _append_status(padded(base, 4, 9), padded(base, 4, 9), padded(far, 2, 9), padded(2 * far, 2, 9), 4, 2, 9, None) == 3
+
+
+def test_rotate_takes_outputs_that_lie_between_one_another():
+    """dq and dk rotated back into the slices of one fused gradient, in the layouts that a model
+    has it in."""
+    n, base, out = 70, 1 << 20, 1 << 30
+    dense = lambda p, h: Rows(p, h * n * 64, n * 64, 64)
+    q, k = dense(base, 8), dense(base + (1 << 24), 2)
+    tok = lambda i, H=12: Rows(out + i * 128, n * H * 64, 64, H * 64)          # [b, n, h + 2g, d]
+    head = lambda i, H=12: Rows(out + i * n * 128, n * H * 64, n * 64, 64)     # [b, h + 2g, n, d]
+    ok = lambda *a, **kw: _rotate_status(*a, n=n, **kw)
+    assert ok(q, k, tok(0), tok(8), 8, 2) == 4 and ok(q, k, tok(4), tok(2), 8, 2) == 4
+    assert ok(q, k, head(0), head(8), 8, 2) == 4
+    assert ok(q, k, tok(0), tok(7), 8, 2) == 1 and ok(q, k, head(1), head(8), 8, 2) == 1
+    assert ok(q, k, tok(0), tok(11), 8, 2) == 1 and ok(q, k, tok(0), head(0), 8, 2) == 1
+    # [b, n, h, 3, d]: a head's q, k and v side by side; from it in place, and into it
+    trio = lambda p, i: Rows(p + i * 128, n * 24 * 64, 192, 24 * 64)
+    for o in (base, out):
+        assert ok(trio(base, 0), trio(base, 1), trio(o, 0), trio(o, 1), 8, 8) == 4
+        assert ok(trio(base, 0), trio(base, 1), trio(o, 0), trio(o, 0), 8, 8) == 1
+    assert ok(trio(base, 0), trio(base, 1), trio(base, 2), trio(out, 1), 8, 8) == 4  # over the values
+    assert ok(trio(base, 0), trio(base, 1), trio(base, 1), trio(out, 1), 8, 8) == 1
+    # bf16 rows between fp32 ones: taken to share, and apart
+    assert ok(tok(0), tok(8), Rows(out, 0, 64, 12 * 32), dense(base, 2), 8, 2, out_dtype=0) == 1
+    assert ok(q, k, dense(out, 8), Rows(out + 8 * n * 64 * 4 * 2, 2 * n * 64, n * 64, 64), 8, 2, out_dtype=0) == 4
+
+
+def test_rotate_accepts_no_rows_that_share_an_element():
+    """Random rows against the elements they cover."""
+    rng = np.random.RandomState(0)
+    cover = lambda r, h, b, n: {r.data // 16 + (i * r.batch_stride + j * r.head_stride + t * r.token_stride) // 8 + e
+                                for i in range(b) for j in range(h) for t in range(n) for e in range(8)}
+    taken = {1: 0, 4: 0}
+    for _ in range(1500):
+        b, g, n = (int(x) for x in rng.randint(1, 4, 3))
+        h = g * int(rng.choice([1, 2]))
+        H = int(rng.randint(h + g, h + 3 * g + 1))
+        perm = rng.permutation(3)
+        size = [b, H, n]
+        stride, s = [0, 0, 0], 64
+        for i in perm:
+            stride[i] = s
+            s *= size[i]
+        rows = lambda i, j=0: Rows((1 << 20) + i * stride[1] * 2 + j * 16, *stride)
+        qo, ko = rows(int(rng.randint(0, H))), rows(int(rng.randint(0, H)), int(rng.choice([0, 0, 0, 1, 7])))
+        if rng.rand() < 0.2:
+            ko.token_stride += 64 * int(rng.randint(1, 9))
+        far = lambda p, h: Rows(p, h * n * 64, n * 64, 64)
+        st = _rotate_status(far(1 << 28, h), far(1 << 29, g), qo, ko, h, g, n, b=b)
+        whole = [cover(qo, h, b, n), cover(ko, g, b, n)]
+        if st == 4:
+            assert not whole[0] & whole[1] and all(len(c) == 8 * x * b * n for c, x in zip(whole, (h, g)))
+        else:
+            assert st == 1
+            if ko.token_stride == qo.token_stride or n == 1 or whole[0] & whole[1]:
+                assert whole[0] & whole[1] or len(whole[0]) < 8 * h * b * n or len(whole[1]) < 8 * g * b * n
+        taken[st] += 1
+    assert min(taken.values()) > 200

@@ -860,3 +860,39 @@ def test_dense_sums_of_a_long_run_are_rounded():
              block_table=torch.arange(n, dtype=torch.int32, device="cuda").repeat(b, 1))
     out, _ = _dense_run(t)
     assert out.float().abs().max() <= 42 * 2.0 ** -24 * (1 + 2.0 ** -8)
+
+
+# ---- rows between rows ------------------------------------------------------
+def test_rotate_into_the_slices_of_a_fused_tensor():
+    """backward's dq and dk rotated back to where the fused projection's gradient has them; the
+    slice of v stays."""
+    b, h, g, n, d = 2, 4, 4, 70, 64
+    f = _freq(d)
+    dq, dk = (_randn(b, x, n, d, dtype=torch.float32, seed=x + i) for i, x in ((80, h), (81, g)))
+    for dt in (torch.float32, torch.bfloat16):
+        want = hils.rotate(dq, f, k=dk, inverse=True, q_out=torch.empty_like(dq, dtype=dt), k_out=torch.empty_like(dk, dtype=dt))
+        for shape, cut in (((b, n, h + 2 * g, d), lambda x, i: x[:, :, (0, h, h + g)[i]:][:, :, :h].transpose(1, 2)),
+                           ((b, h + 2 * g, n, d), lambda x, i: x[:, (0, h, h + g)[i]:][:, :h]),
+                           ((b, n, h, 3, d), lambda x, i: x[:, :, :, i].transpose(1, 2))):
+            x = torch.full(shape, 7.0, dtype=dt, device="cuda")
+            hils.rotate(dq, f, k=dk, inverse=True, q_out=cut(x, 0), k_out=cut(x, 1))
+            assert torch.equal(cut(x, 0), want[0]) and torch.equal(cut(x, 1), want[1]) and (cut(x, 2) == 7).all()
+            # and forward again, in place
+            again = hils.rotate(*(y.clone() for y in want[:1]), f, k=want[1].clone())
+            hils.rotate(cut(x, 0), f, k=cut(x, 1), q_out=cut(x, 0), k_out=cut(x, 1))
+            assert torch.equal(cut(x, 0), again[0]) and torch.equal(cut(x, 1), again[1]) and (cut(x, 2) == 7).all()
+
+
+def test_append_rotates_queries_in_the_fused_projection():
+    b, h, g, d = 3, 4, 2, 64
+    fused = _randn(b, h + 2 * g, d, dtype=torch.bfloat16, seed=83)
+    ref = fused.clone()
+    i = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    f, lens, table = _freq(d), i(70, 1, 64), i(0, 1, 2, 3, 4, 5).view(3, 2)
+    kp, vp = (torch.zeros(6, g, 64, d, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    kq, vq = kp.clone(), vp.clone()
+    want = hils.append_paged(ref[:, h:h + g], ref[:, h + g:], kp, vp, table, lens, inv_freq=f, q=ref[:, :h])
+    got = hils.append_paged(fused[:, h:h + g], fused[:, h + g:], kq, vq, table, lens, inv_freq=f, q=fused[:, :h],
+                            q_out=fused[:, :h])
+    assert torch.equal(got, want) and torch.equal(fused[:, h:], ref[:, h:])
+    assert torch.equal(kp, kq) and torch.equal(vp, vq)
