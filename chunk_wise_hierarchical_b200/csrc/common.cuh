@@ -82,7 +82,10 @@ __device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long v)
 // Kernels launched by launch_overlapped may come onto the SMs while the kernel before them in the
 // stream still runs: they begin with this wait, and touch no memory before it.  It returns when
 // that kernel has completed and its writes are visible, so the stream's order holds; what is
-// gained is the launch itself.  Their own successors may come as early.
+// gained is the launch itself.  Their own successors may come as early.  The wait orders ordinary
+// loads.  Loads through the read-only path (__ldg, const __restrict__ pointers) are not for these
+// kernels: they ask that nobody writes the data from the kernel's start on, and the kernel before
+// may be writing it (the q of a dense decode is what an append has just rotated).
 __device__ __forceinline__ void wait_for_stream() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

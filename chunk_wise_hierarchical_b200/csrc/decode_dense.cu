@@ -184,8 +184,8 @@ struct WarpStateBf16 {
                                                             ((size_t)bi * a.h + gi * G + (lane >> 2) % G) * D);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      q[k][0] = __ldg(row + k * 8 + (lane & 3));
-      q[k][1] = __ldg(row + k * 8 + 4 + (lane & 3));
+      q[k][0] = row[k * 8 + (lane & 3)];
+      q[k][1] = row[k * 8 + 4 + (lane & 3)];
       o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
     }
     m[0] = m[1] = -INFINITY;
@@ -353,7 +353,7 @@ struct WarpStateF32 {
 
   __device__ void start(const DenseArgs& a, int bi, int gi, float* sq, int lane) {
     const float* row = static_cast<const float*>(a.q) + ((size_t)bi * a.h + gi * G) * D;
-    for (int x = lane; x < G * D; x += 32) sq[x] = __ldg(row + x);
+    for (int x = lane; x < G * D; x += 32) sq[x] = row[x];
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < NH; ++j) {

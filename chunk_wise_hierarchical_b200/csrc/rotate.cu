@@ -101,7 +101,7 @@ struct Turns {
     if (how == kCopied) return;
 #pragma unroll
     for (int i = 0; i < E; ++i) {  // pair u E + i, whichever way the pairs are laid out
-      w[i] = turn_of(pos, __ldg(inv_freq + u * E + i));
+      w[i] = turn_of(pos, inv_freq[u * E + i]);
       if (inverse) w[i].y = -w[i].y;
     }
   }

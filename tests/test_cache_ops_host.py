@@ -481,3 +481,15 @@ def test_rotate_accepts_no_rows_that_share_an_element():
                 assert whole[0] & whole[1] or len(whole[0]) < 8 * h * b * n or len(whole[1]) < 8 * g * b * n
         taken[st] += 1
     assert min(taken.values()) > 200
+
+
+def test_kernels_that_start_early_read_through_the_ordinary_path():
+    """A kernel that may run beside its predecessor (wait_for_stream) must not use loads that ask
+    for data nobody writes during its life."""
+    import pathlib
+    src = pathlib.Path(_abi.__file__).parent / "csrc"
+    early = [p for p in sorted(src.glob("*.cu")) if "wait_for_stream();" in p.read_text()]
+    assert {p.name for p in early} >= {"decode_dense.cu", "rotate.cu"}
+    for p in early:
+        for word in ("__ldg(", "ld.global.nc", "__restrict__"):
+            assert word not in p.read_text(), f"{p.name}: {word}"

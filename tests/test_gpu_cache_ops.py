@@ -896,3 +896,52 @@ def test_append_rotates_queries_in_the_fused_projection():
                             q_out=fused[:, :h])
     assert torch.equal(got, want) and torch.equal(fused[:, h:], ref[:, h:])
     assert torch.equal(kp, kq) and torch.equal(vp, vq)
+
+
+# ---- kernels that start while their predecessor runs ------------------------
+def test_inputs_that_the_kernel_before_has_just_written():
+    """A rotation writes the frequencies that the next rotation and append read, the append the
+    queries that the dense decode reads: captured, and replayed with other values each time."""
+    b, h, g, d = 4, 8, 2, 64
+    i = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    t, _ = _dense_case([700, 129, 2000, 1], h, g, d, "bf16", seed=90)
+    m = t["block_table"].shape[1]
+    first = _freq(d)
+    raw = torch.empty(1, 1, 1, d, device="cuda")               # its rotated row's head: the frequencies
+    row, freq = torch.empty_like(raw), None
+    freq = row.view(-1)[:d // 2]
+    fused, q = torch.empty(b, h + 2 * g, d, dtype=torch.bfloat16, device="cuda"), torch.empty_like(t["q"])
+    turned = torch.empty(1, h, b, d, dtype=torch.bfloat16, device="cuda")
+    app = hils.Append(b, h, g, d, m, torch.bfloat16, inv_freq=freq)
+    dense = hils.DenseDecode(b, h, g, d, m, torch.bfloat16)
+    pos, out, n = i(3), torch.empty_like(q), t["seq_lens"]
+
+    def step():
+        for _ in range(3):
+            hils.rotate(raw, first, positions=pos, q_out=row)
+            hils.rotate(fused[None, :, :h].transpose(1, 2), freq, positions=n, q_out=turned)
+            app(fused[:, h:h + g], fused[:, h + g:], t["k_pages"], t["v_pages"], t["block_table"], n, q=fused[:, :h], q_out=q)
+            dense(q, t["k_pages"], t["v_pages"], t["block_table"], n, out=out)
+
+    raw.fill_(0.1)
+    fused.zero_()
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for s in range(4):
+        raw.copy_(_randn(1, 1, 1, d, dtype=torch.float32, seed=91 + s))
+        fused.copy_(_randn(b, h + 2 * g, d, dtype=torch.bfloat16, seed=95 + s))
+        graph.replay()
+        torch.cuda.synchronize()
+        f = hils.rotate(raw, first, positions=pos).view(-1)[:d // 2].clone()
+        torch.cuda.synchronize()
+        assert torch.equal(f, freq)
+        assert torch.equal(turned, hils.rotate(fused[None, :, :h].transpose(1, 2), f, positions=n))
+        kp, vp = t["k_pages"].clone(), t["v_pages"].clone()
+        torch.cuda.synchronize()
+        qs = hils.append_paged(fused[:, h:h + g], fused[:, h + g:], kp, vp, t["block_table"], n, inv_freq=f, q=fused[:, :h])
+        torch.cuda.synchronize()
+        assert torch.equal(q, qs) and torch.equal(kp, t["k_pages"]) and torch.equal(vp, t["v_pages"])
+        assert torch.equal(out, _dense_run({**t, "q": q.clone()})[0])
