@@ -945,3 +945,46 @@ def test_inputs_that_the_kernel_before_has_just_written():
         torch.cuda.synchronize()
         assert torch.equal(q, qs) and torch.equal(kp, t["k_pages"]) and torch.equal(vp, t["v_pages"])
         assert torch.equal(out, _dense_run({**t, "q": q.clone()})[0])
+
+
+def test_captured_behind_writes_that_change_with_every_replay():
+    """Positions written by a second stream that joins late, and a workspace whose counters another
+    stream's call left dirty until a node of the graph clears it: a call that overtakes either
+    shows."""
+    t, _ = _dense_case([2000, 700, 0], 8, 2, 64, "bf16", seed=22)
+    f = _freq(64)
+    x = _randn(3, 8, 1, 64, dtype=torch.bfloat16, seed=40)
+    pos, new_pos = (torch.zeros(3, 1, dtype=torch.int32, device="cuda") for _ in range(2))
+    side = torch.cuda.Stream()
+    q, out = torch.empty_like(t["q"]), torch.empty_like(t["q"])
+    big = torch.randn(1 << 24, device="cuda")
+    from chunk_wise_hierarchical_b200._abi import make_shape, workspace_size
+    m = t["block_table"].shape[1]
+    ws = torch.zeros(workspace_size(make_shape(3, 8, 2, 64, m * 64, 0, 1), hils.OP_DECODE_DENSE), dtype=torch.uint8, device="cuda")
+    call = hils.DenseDecode(3, 8, 2, 64, m, torch.bfloat16, ws=ws)
+
+    def step():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            z = (big * 2).sin_().sum() * 0                # long enough to be overtaken
+            pos.copy_(new_pos + z.int())
+            ws.zero_()
+        main.wait_stream(side)
+        hils.rotate(x, f, positions=pos, q_out=q.view(3, 8, 1, 64))
+        call(**{**t, "q": q}, out=out)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for s in range(3):
+        new_pos.copy_(torch.tensor([[1999 + s], [3 * s], [100 * s]], dtype=torch.int32))
+        pos.fill_(-77)
+        ws.fill_(1)  # counters that no join would find its last part by
+        graph.replay()
+        torch.cuda.synchronize()
+        want = hils.rotate(x, f, positions=new_pos.clone())
+        assert torch.equal(q, want[:, :, 0])
+        assert torch.equal(out, _dense_run({**t, "q": q.clone()})[0]) and call.device_status() == 0
