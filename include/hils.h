@@ -395,8 +395,8 @@ typedef struct {
  *   inv_freq     [rotary_dim / 2] fp32, device
  *   rotary_dim   a multiple of 16, 16 <= rotary_dim <= head_dim
  *   interleaved  0: pair f is (f, f + rotary_dim / 2); 1: pair f is (2f, 2f + 1)
- * Angles are reduced in fp64 (position * inv_freq is exact to far below an fp32 step at any
- * int32 position), the products are fp32, and each output is rounded once. */
+ * Angles are reduced in fp64 (their remainder is exact to far below an fp32 step at any int32
+ * position and frequency up to 1), the products are fp32, and each output is rounded once. */
 typedef struct {
   const float* inv_freq;
   int32_t rotary_dim;

@@ -988,3 +988,26 @@ def test_captured_behind_writes_that_change_with_every_replay():
         want = hils.rotate(x, f, positions=new_pos.clone())
         assert torch.equal(q, want[:, :, 0])
         assert torch.equal(out, _dense_run({**t, "q": q.clone()})[0]) and call.device_status() == 0
+
+
+def test_rotate_angles_at_the_farthest_positions():
+    """(1, 0) turned by p w, near the largest int32 p, against exact rationals: the remainder 2 t
+    (half turns, at most 1) is rounded to fp32, pi 2^-25 of angle, and sincospif is good to 2 steps
+    of 2^-24; 1 cos - 0 sin and 0 cos + 1 sin are exact."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    pi = Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+    rng = np.random.RandomState(0)
+    w = torch.from_numpy(rng.uniform(0.5, 1, 32).astype(np.float32))
+    p = torch.from_numpy(2**31 - 1 - rng.randint(0, 1 << 20, 64)).int()
+    p[::2] = -p[::2]
+    x = torch.zeros(1, 1, 64, 64, device="cuda")
+    x[..., :32] = 1
+    got = _np(hils.rotate(x, w.cuda(), positions=p.cuda()))[0, 0]
+    want = np.empty((64, 64))
+    for i, a in enumerate(p.tolist()):
+        for j, b in enumerate(w.tolist()):
+            turns = Decimal(a) * Decimal(b) / (2 * pi)
+            ang = float((turns - turns.to_integral_value()) * 2 * pi)
+            want[i, j], want[i, 32 + j] = math.cos(ang), math.sin(ang)
+    assert np.abs(got - want).max() <= math.pi * 2.0 ** -25 + 2.0 ** -23
