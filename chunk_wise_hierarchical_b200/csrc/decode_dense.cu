@@ -87,7 +87,6 @@ struct DenseCfg {
   static constexpr int kP = sizeof(T) == 4 ? (kTile + 4) * G : 0;
   static constexpr size_t kSmem = 1024 + (size_t)kRings + 4ull * (kHeads + kWeights + kSums + kDenseWarps * (kQ + kP));
   static_assert(kStages >= 1 && kTile % 16 == 0 && G * D * 4 <= kDenseRing, "a unit fills a stage, an output fits one");
-  static_assert(kSmem <= 227 * 1024 - 10 * 1024, "room for the static shared variables");
 };
 
 struct alignas(64) DenseKernelArgs {
@@ -573,6 +572,11 @@ __global__ void __launch_bounds__(kDenseThreads, 1) decode_dense_kernel(const __
   __shared__ float2 s_ml[2 * kDenseWarps][G];
   __shared__ float s_M[G], s_z[G];
   __shared__ int s_abort, s_last[2];
+  static_assert(C::kSmem + sizeof(s_prefix) + sizeof(s_len) + sizeof(s_own_prefix) + sizeof(s_own_len) + sizeof(s_scan) +
+                        sizeof(s_full) + sizeof(s_seg) + sizeof(s_cut) + sizeof(s_ml) + sizeof(s_M) + sizeof(s_z) +
+                        sizeof(s_abort) + sizeof(s_last) + 12 * 16 <=
+                    227 * 1024,
+                "dynamic and static shared memory of a CTA, the gaps between variables among them");
 
   const DenseArgs& a = ka.a;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
