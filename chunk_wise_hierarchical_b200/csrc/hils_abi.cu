@@ -22,12 +22,13 @@ constexpr size_t kAlign = 256;
 constexpr size_t kHeader = 256;  // error word + reserved
 constexpr int kMaxWindow = 64 * 128;  // local branch of at most 128 chunks
 constexpr int kMaxDecodeLocal = 16;   // ... and of at most 16 in a decode step
+constexpr int kAnyWindow = 0x7fffffff;  // dense decode: a window only says where it begins
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-hils_status check_shape(const hils_shape* s, bool need_seq) {
+hils_status check_shape(const hils_shape* s, bool need_seq, int max_window = kMaxWindow) {
   if (!s) return HILS_ERR_INVALID_ARG;
   if (s->batch < 0 || s->heads_q <= 0 || s->heads_kv <= 0 || s->head_dim <= 0 || s->seq_len < 0 ||
       s->chunk <= 0 || s->top_k < 0)
@@ -41,7 +42,7 @@ hils_status check_shape(const hils_shape* s, bool need_seq) {
   if (s->chunk != hils::kChunk) return HILS_ERR_UNSUPPORTED;
   if (s->top_k > hils::kMaxTopK) return HILS_ERR_UNSUPPORTED;
   if (s->window < 0 || s->window % s->chunk != 0) return HILS_ERR_INVALID_ARG;
-  if (s->window > kMaxWindow) return HILS_ERR_UNSUPPORTED;
+  if (s->window > max_window) return HILS_ERR_UNSUPPORTED;
   (void)need_seq;
   return HILS_OK;
 }
@@ -326,7 +327,7 @@ uint32_t hils_set_wait_limit(uint32_t polls) { return g_wait_limit.exchange(poll
 
 hils_status hils_workspace_size(const hils_shape* s, int32_t op, size_t* bytes) {
   if (!bytes) return HILS_ERR_INVALID_ARG;
-  hils_status st = check_shape(s, true);
+  hils_status st = check_shape(s, true, op == HILS_OP_DECODE_DENSE ? kAnyWindow : kMaxWindow);
   if (st != HILS_OK) return st;
   switch (op) {
     case HILS_OP_SELECT: *bytes = kHeader + gtc_bytes(s); return HILS_OK;
@@ -675,7 +676,7 @@ hils_status hils_append_paged(const hils_shape* s, const hils_rows* k, const hil
 hils_status hils_decode_dense(const hils_shape* s, const void* q, const void* k_pages, const void* v_pages,
                               const int32_t* block_table, int32_t max_chunks, const int32_t* seq_lens,
                               int32_t n_pages, void* out, float* lse_out, void* ws, size_t ws_bytes, void* stream) {
-  hils_status st = check_shape(s, true);
+  hils_status st = check_shape(s, true, kAnyWindow);
   if (st != HILS_OK) return st;
   if (s->batch == 0) return HILS_OK;
   if (max_chunks <= 0 || n_pages <= 0) return HILS_ERR_INVALID_ARG;

@@ -487,8 +487,8 @@ HILS_API hils_status hils_append_paged(const hils_shape* shape, const hils_rows*
  * anything, NaN included.  An infinite value before it gives that infinity where its weight
  * is above 2^-100 of the largest, NaN where its weight is zero.  Page ids outside [0, n_pages)
  * are skipped and flagged, and so are the keys of a length beyond max_chunks * B.
- * heads_kv * max_chunks is limited to 2^29 and n_pages * heads_kv to 2^31; beyond them, and
- * for a window above 128 chunks, the call returns HILS_ERR_UNSUPPORTED.
+ * heads_kv * max_chunks is limited to 2^29 and n_pages * heads_kv to 2^31; beyond them the call
+ * returns HILS_ERR_UNSUPPORTED.
  */
 HILS_API hils_status hils_decode_dense(const hils_shape* shape, const void* q, const void* k_pages,
                                        const void* v_pages, const int32_t* block_table, int32_t max_chunks,

@@ -493,3 +493,14 @@ def test_kernels_that_start_early_read_through_the_ordinary_path():
     for p in early:
         for word in ("__ldg(", "ld.global.nc", "__restrict__"):
             assert word not in p.read_text(), f"{p.name}: {word}"
+
+
+def test_dense_takes_any_window():
+    """The limit of 128 chunks is the prefill kernels'."""
+    L, ref, n = hils.lib(), ctypes.byref, ctypes.c_size_t(0)
+    for w, other in ((64 * 128, 0), (64 * 129, 2), (1 << 30, 2)):
+        s = _sh(window=w, seq_len=640)
+        assert L.hils_workspace_size(ref(s), hils.OP_DECODE_DENSE, ref(n)) == 0
+        assert L.hils_decode_dense(ref(s), FAKE, FAKE, FAKE, FAKE, 10, FAKE, 4, FAKE, None, None, n.value, None) == 3
+        for op in (hils.OP_ATTEND, hils.OP_DECODE, hils.OP_APPEND):
+            assert L.hils_workspace_size(ref(s), op, ref(n)) == other

@@ -1011,3 +1011,12 @@ def test_rotate_angles_at_the_farthest_positions():
             ang = float((turns - turns.to_integral_value()) * 2 * pi)
             want[i, j], want[i, 32 + j] = math.cos(ang), math.sin(ang)
     assert np.abs(got - want).max() <= math.pi * 2.0 ** -25 + 2.0 ** -23
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [64 * 128, 64 * 129, 64 * 1000, 64 * ((1 << 25) - 1)])
+def test_dense_wide_windows(dtype, window):
+    lens = [64 * 129 + 5, 20000, 70001, 0, 64 * 130, 100]
+    t, _ = _dense_case(lens, 4, 2, 64, dtype, seed=85)
+    out, lse = _dense_run(t, window=window)
+    _dense_close_gpu(out, lse, t, lens, window)
