@@ -27,6 +27,7 @@ constexpr int kAnyWindow = 0x7fffffff;  // dense decode: a window only says wher
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 hils_status check_shape(const hils_shape* s, bool need_seq, int max_window = kMaxWindow) {
   if (!s) return HILS_ERR_INVALID_ARG;
@@ -293,7 +294,7 @@ bool in_place(const hils_rows* out, const hils_rows* in, long long nb, long long
          (nh <= 1 || out->head_stride == in->head_stride) && (nt <= 1 || out->token_stride == in->token_stride);
 }
 hils_status check_rope(const hils_rope* r, int head_dim) {
-  if (!r || !r->inv_freq || (reinterpret_cast<uintptr_t>(r->inv_freq) & 3u) != 0) return HILS_ERR_INVALID_ARG;
+  if (!r || !r->inv_freq || !aligned4(r->inv_freq)) return HILS_ERR_INVALID_ARG;
   if (r->rotary_dim <= 0 || r->rotary_dim > head_dim || (r->interleaved != 0 && r->interleaved != 1))
     return HILS_ERR_INVALID_ARG;
   return r->rotary_dim % 16 == 0 ? HILS_OK : HILS_ERR_UNSUPPORTED;
@@ -573,7 +574,7 @@ hils_status hils_rotate(const hils_shape* s, const hils_rows* q, const hils_rows
   if (st != HILS_OK) return st;
   if (out_dtype != HILS_F32 && out_dtype != HILS_BF16) return HILS_ERR_INVALID_ARG;
   if ((k == nullptr) != (k_out == nullptr)) return HILS_ERR_INVALID_ARG;
-  if (position_stride < 0) return HILS_ERR_INVALID_ARG;
+  if (position_stride < 0 || !aligned4(positions)) return HILS_ERR_INVALID_ARG;
   if ((st = check_rope(rope, s->head_dim)) != HILS_OK) return st;
   if ((size_t)s->batch * s->seq_len == 0) return HILS_OK;
   if ((long long)s->batch * s->seq_len > 0x7fffffffll) return HILS_ERR_UNSUPPORTED;
@@ -623,6 +624,8 @@ hils_status hils_append_paged(const hils_shape* s, const hils_rows* k, const hil
   if (max_chunks <= 0 || n_pages <= 0) return HILS_ERR_INVALID_ARG;
   if (max_chunks > (0x7fffffff / s->chunk)) return HILS_ERR_UNSUPPORTED;  // positions are 32-bit
   if (!seq_lens || !block_table) return HILS_ERR_INVALID_ARG;
+  if (!aligned4(seq_lens) || !aligned4(block_table) || !aligned4(cu_new) || !aligned4(new_lens) || !aligned4(full_pages))
+    return HILS_ERR_INVALID_ARG;
   const size_t es = elem_size(s->dtype);
   if (tokens > 0) {
     if (!k_pages || !v_pages || !aligned16(k_pages) || !aligned16(v_pages)) return HILS_ERR_INVALID_ARG;
@@ -683,6 +686,7 @@ hils_status hils_decode_dense(const hils_shape* s, const void* q, const void* k_
   if ((long long)max_chunks > ((long long)s->seq_len + s->chunk - 1) / s->chunk) return HILS_ERR_INVALID_ARG;
   if (!q || !k_pages || !v_pages || !block_table || !seq_lens || !out) return HILS_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out)) return HILS_ERR_INVALID_ARG;
+  if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(lse_out)) return HILS_ERR_INVALID_ARG;
   if (!hils::decode_dense_supported(s->heads_kv, max_chunks, n_pages)) return HILS_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < dense_bytes(s) || !aligned16(ws)) return HILS_ERR_WORKSPACE;
   hils::DenseArgs a{};

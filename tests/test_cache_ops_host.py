@@ -504,3 +504,29 @@ def test_dense_takes_any_window():
         assert L.hils_decode_dense(ref(s), FAKE, FAKE, FAKE, FAKE, 10, FAKE, 4, FAKE, None, None, n.value, None) == 3
         for op in (hils.OP_ATTEND, hils.OP_DECODE, hils.OP_APPEND):
             assert L.hils_workspace_size(ref(s), op, ref(n)) == other
+
+
+def test_int_arrays_off_their_alignment_are_refused():
+    """A 4-byte load from such an address would fault on the GPU."""
+    L, ref, odd = hils.lib(), ctypes.byref, P_((1 << 20) + 2)
+    s, ro = _sh(), Rope(1 << 20, 32, 0)
+    far = lambda i, h: Rows((i + 1) << 28, h * 4 * 64, 4 * 64, 64)
+    k, v = far(0, 2), far(1, 2)
+
+    def append(cu=None, nl=None, sl=FAKE, bt=FAKE, fp=None):
+        return L.hils_append_paged(ref(s), ref(k), ref(v), None, None, 4, cu, nl, sl, bt, 4, 4, ref(ro), P_(5 << 28),
+                                   P_(6 << 28), fp, None, 256, None)
+
+    assert append() == 3 and append(nl=FAKE, fp=FAKE) == 3 and append(cu=FAKE) == 3
+    assert [append(**{x: odd}) for x in ("cu", "nl", "sl", "bt", "fp")] == [1] * 5
+    n = ctypes.c_size_t(0)
+    L.hils_workspace_size(ref(s), hils.OP_DECODE_DENSE, ref(n))
+
+    def dense(bt=FAKE, sl=FAKE, lse=None):
+        return L.hils_decode_dense(ref(s), P_(1 << 28), P_(2 << 28), P_(3 << 28), bt, 10, sl, 4, P_(4 << 28), lse, None,
+                                   n.value, None)
+
+    assert dense() == 3 and dense(lse=P_(5 << 28)) == 3
+    assert [dense(**{x: odd}) for x in ("bt", "sl", "lse")] == [1] * 3
+    r = Rows(1 << 28, 8 * 640 * 64, 640 * 64, 64)
+    assert L.hils_rotate(ref(s), ref(r), None, ref(ro), odd, 0, 0, ref(r), None, 1, None) == 1
