@@ -646,6 +646,8 @@ def rotate(q, inv_freq, k=None, positions=None, inverse=False, interleaved=False
                 (_shape_of(b, h, g, d, n, 0, bf16), _rows4(q), None if ks is None else _rows4(k), rope,
                  None if positions is None else positions.data_ptr(), pstride, 1 if inverse else 0, _rows4(q_out),
                  None if ks is None else _rows4(k_out), out_bf16), q, dev, stream, "hils_rotate")
+    elif b * n and h + g:
+        raise ValueError("q and k must have heads, both or neither")
     return q_out if ks is None else (q_out, k_out)
 
 

@@ -530,3 +530,11 @@ def test_int_arrays_off_their_alignment_are_refused():
     assert [dense(**{x: odd}) for x in ("bt", "sl", "lse")] == [1] * 3
     r = Rows(1 << 28, 8 * 640 * 64, 640 * 64, 64)
     assert L.hils_rotate(ref(s), ref(r), None, ref(ro), odd, 0, 0, ref(r), None, 1, None) == 1
+
+
+def test_rotate_refuses_one_tensor_without_heads():
+    q, k, f = torch.zeros(B, H, N, D, dtype=BF), torch.zeros(B, G, N, D, dtype=BF), torch.ones(16)
+    _refused(hils.rotate, q, f, k=k[:, :0])
+    _refused(hils.rotate, q[:, :0], f, k=k)
+    assert hils.rotate(q[:, :0], f).shape == (B, 0, N, D)
+    assert [x.shape[1] for x in hils.rotate(q[:, :0], f, k=k[:, :0])] == [0, 0]
