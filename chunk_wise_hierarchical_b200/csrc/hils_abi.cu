@@ -619,7 +619,10 @@ hils_status hils_append_paged(const hils_shape* s, const hils_rows* k, const hil
   if (n_new < 0 || (q == nullptr) != (q_out == nullptr) || (cu_new && new_lens)) return HILS_ERR_INVALID_ARG;
   if (rope && (st = check_rope(rope, s->head_dim)) != HILS_OK) return st;
   const long long tokens = cu_new ? n_new : (long long)s->batch * n_new;
-  if (s->batch == 0) return HILS_OK;
+  if (s->batch == 0) {  // every row is padding: no page is filled
+    if (!full_pages || tokens < s->chunk) return HILS_OK;
+    return cuda_status(cudaMemsetAsync(full_pages, 0xff, (size_t)(tokens / s->chunk) * 4, (cudaStream_t)stream));
+  }
   if (tokens > 0x7fffffffll) return HILS_ERR_UNSUPPORTED;
   if (max_chunks <= 0 || n_pages <= 0) return HILS_ERR_INVALID_ARG;
   if (max_chunks > (0x7fffffff / s->chunk)) return HILS_ERR_UNSUPPORTED;  // positions are 32-bit

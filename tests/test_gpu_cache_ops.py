@@ -1020,3 +1020,13 @@ def test_dense_wide_windows(dtype, window):
     t, _ = _dense_case(lens, 4, 2, 64, dtype, seed=85)
     out, lse = _dense_run(t, window=window)
     _dense_close_gpu(out, lse, t, lens, window)
+
+
+def test_append_for_no_sequences_lists_no_pages():
+    call = hils.Append(0, 2, 2, 64, 3, torch.bfloat16)
+    k = torch.zeros(130, 2, 64, dtype=torch.bfloat16, device="cuda")
+    pages = torch.zeros(4, 2, 64, 64, dtype=torch.bfloat16, device="cuda")
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+    full = torch.full((hils.append_slots(0, 130),), 99, dtype=torch.int32, device="cuda")
+    call(k, k, pages, pages.clone(), i(0, 3), i(0), cu_new=i(1), full_pages=full)
+    assert full.tolist() == [-1, -1]
