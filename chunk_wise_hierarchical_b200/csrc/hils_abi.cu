@@ -691,6 +691,18 @@ hils_status hils_decode_dense(const hils_shape* s, const void* q, const void* k_
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out)) return HILS_ERR_INVALID_ARG;
   if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(lse_out)) return HILS_ERR_INVALID_ARG;
   if (!hils::decode_dense_supported(s->heads_kv, max_chunks, n_pages)) return HILS_ERR_UNSUPPORTED;
+  {
+    auto span = [](const void* p, size_t bytes) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(p);
+      return Span{x, x + bytes};
+    };
+    const size_t es = elem_size(s->dtype), row = (size_t)s->head_dim * es, nr = (size_t)s->batch * s->heads_q;
+    const size_t pool = (size_t)n_pages * s->heads_kv * s->chunk * row;
+    const Span o = span(out, nr * row), l = span(lse_out, lse_out ? nr * 4 : 0);
+    for (const Span& in : {span(k_pages, pool), span(v_pages, pool), span(q, nr * row)})
+      if (overlap(l, in) || (overlap(o, in) && o.lo != reinterpret_cast<uintptr_t>(q))) return HILS_ERR_INVALID_ARG;
+    if (overlap(o, l)) return HILS_ERR_INVALID_ARG;
+  }
   if (!ws || ws_bytes < dense_bytes(s) || !aligned16(ws)) return HILS_ERR_WORKSPACE;
   hils::DenseArgs a{};
   a.q = q; a.k_pages = k_pages; a.v_pages = v_pages; a.block_table = block_table; a.seq_lens = seq_lens;

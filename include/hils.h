@@ -474,8 +474,10 @@ HILS_API hils_status hils_append_paged(const hils_shape* shape, const hils_rows*
  *                token, keys from (floor((seq_lens[b] - 1) / B) + 1 - W / B) * B on -- the
  *                local branch that hils_decode takes for the same window (here W = B is the
  *                own chunk alone, and 0 is not).  shape.top_k is not read
- *   out          [batch, heads_q, head_dim] (dtype), written
- *   lse_out      [batch, heads_q] fp32 or NULL: log of the sum of exp(logit) over the keys
+ *   out          [batch, heads_q, head_dim] (dtype), written; may be q's own memory
+ *   lse_out      [batch, heads_q] fp32 or NULL: log of the sum of exp(logit) over the keys.
+ *                Any other overlap of out or lse_out with q, the pages or each other is
+ *                refused
  *   ws           workspace of hils_workspace_size(HILS_OP_DECODE_DENSE) bytes, zero-filled
  *                before first use and before it serves another shape: the error word,
  *                partial sums and the counters of their parts, which every call leaves at

@@ -538,3 +538,20 @@ def test_rotate_refuses_one_tensor_without_heads():
     _refused(hils.rotate, q[:, :0], f, k=k)
     assert hils.rotate(q[:, :0], f).shape == (B, 0, N, D)
     assert [x.shape[1] for x in hils.rotate(q[:, :0], f, k=k[:, :0])] == [0, 0]
+
+
+def test_dense_refuses_outputs_on_its_inputs():
+    L, ref, n = hils.lib(), ctypes.byref, ctypes.c_size_t(0)
+    s = _sh()  # q and out 2 KB, a pool of four pages 64 KB, lse 64 bytes
+    L.hils_workspace_size(ref(s), hils.OP_DECODE_DENSE, ref(n))
+
+    def call(out=5 << 20, lse=None, q=1 << 20):
+        return L.hils_decode_dense(ref(s), P_(q), P_(2 << 20), P_(3 << 20), FAKE, 10, FAKE, 4, P_(out),
+                                   lse and P_(lse), None, n.value, None)
+
+    assert call() == 3 and call(out=1 << 20) == 3 and call(lse=6 << 20) == 3
+    assert call(out=(5 << 20) - 16, lse=(5 << 20) + 2032) == 3
+    for kw in (dict(out=(1 << 20) + 16), dict(out=(1 << 20) - 16), dict(out=2 << 20), dict(out=(3 << 20) + 65520),
+               dict(lse=5 << 20), dict(lse=(5 << 20) + 2044), dict(lse=(1 << 20) + 4), dict(lse=2 << 20),
+               dict(out=1 << 20, lse=(1 << 20) + 64)):
+        assert call(**kw) == 1, kw

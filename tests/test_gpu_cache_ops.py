@@ -1030,3 +1030,15 @@ def test_append_for_no_sequences_lists_no_pages():
     full = torch.full((hils.append_slots(0, 130),), 99, dtype=torch.int32, device="cuda")
     call(k, k, pages, pages.clone(), i(0, 3), i(0), cu_new=i(1), full_pages=full)
     assert full.tolist() == [-1, -1]
+
+
+@pytest.mark.parametrize("dtype,h,g", [("bf16", 8, 2), ("f32", 2, 2)])
+def test_dense_in_place(dtype, h, g):
+    """out may be q itself: cut between warps and SMs, whole, and empty."""
+    t, _ = _dense_case([9000, 5, 0, 700, 64], h, g, 128, dtype, seed=86)
+    want, lse = _dense_run(t)
+    call = hils.DenseDecode(5, h, g, 128, t["block_table"].shape[1], t["q"].dtype)
+    for _ in range(3):
+        q, l = t["q"].clone(), torch.empty_like(lse)
+        assert call(**{**t, "q": q}, out=q, lse=l) is q
+        assert torch.equal(q, want) and torch.equal(l, lse)
