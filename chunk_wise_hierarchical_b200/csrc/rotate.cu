@@ -29,8 +29,8 @@ namespace {
 constexpr int kRotThreads = 128;
 constexpr int kRotHeads = 4;       // heads whose loads a thread issues before it stores the first
 constexpr int kRotMany = 32 * 148; // CTAs wanted: several waves, so that the last one costs little ...
-constexpr int kRotBlock = 8;       // ... with blocks of this many heads or more (the angles are computed per block)
-constexpr int kRotFew = 2 * 148;   // CTAs wanted for few tokens, down to one head each
+constexpr int kRotBlock = 8;       // ... but blocks of this many heads (the angles are computed per block) ...
+constexpr int kRotFew = 2 * 148;   // ... unless that leaves fewer CTAs than this: then down to one head each
 constexpr int kRotSeqs = 1024;     // sequences whose row offsets fit shared memory
 
 __device__ __forceinline__ float2 turn_of(int pos, float w) {
@@ -165,15 +165,18 @@ __device__ __forceinline__ void turn_heads(const Tin* src, long long ss, Tout* d
   }
 }
 
-// Heads per CTA.  One block of all heads computes the angles once but leaves few waves of CTAs:
-// at the 345M prefill shape 80 us in an earlier form against 47 with blocks of 8; now 46 us with
-// blocks of 16 heads, 44 with 8, and with 8 waves wanted instead of 32 45 us there and 88 instead
-// of 80 for 20K prompt tokens.  Few tokens are spread further, down to one head a CTA: one token
-// for each of 64 sequences 3.6 us, 4.0 with all heads in one block.
+// Heads per CTA.  One block of all heads computes the angles once but leaves few waves of CTAs: at
+// the 345M prefill shape 46 us with blocks of 16 heads, 44 with 8, and with 8 waves wanted instead
+// of 32 45 us there and 88 instead of 80 for 20K prompt tokens.  Halves that are not below
+// kRotBlock are tried first, then kRotBlock itself: 48 heads of those prompts take blocks of 12
+// (80.5 us, 81.8 with 8), 40 heads of a 2K prompt blocks of 8 (8.1 us; halved on to 5 9.2), 48
+// heads of four prompts 8.3 us (6: 10.7).  Few tokens are spread further, down to one head a CTA:
+// one token for each of 64 sequences 3.6 us, 4.0 with all heads in one block.
 int pick_heads(long long token_blocks, int heads) {
   int hb = heads;
   auto ctas = [&] { return token_blocks * ((heads + hb - 1) / hb); };
-  while (hb > kRotBlock && ctas() < kRotMany) hb = (hb + 1) / 2;
+  while ((hb + 1) / 2 >= kRotBlock && ctas() < kRotMany) hb = (hb + 1) / 2;
+  if (hb > kRotBlock && ctas() < kRotMany) hb = kRotBlock;
   while (hb > 1 && ctas() < kRotFew) hb = (hb + 1) / 2;
   return hb;
 }

@@ -1042,3 +1042,15 @@ def test_dense_in_place(dtype, h, g):
         q, l = t["q"].clone(), torch.empty_like(lse)
         assert call(**{**t, "q": q}, out=q, lse=l) is q
         assert torch.equal(q, want) and torch.equal(l, lse)
+
+
+@pytest.mark.parametrize("h,g,n", [(8, 1, 40), (32, 8, 40), (32, 8, 600), (32, 8, 5000), (24, 3, 6000), (9, 9, 5000)])
+def test_rotate_blocks_of_heads(h, g, n):
+    """However the heads are dealt to blocks, each is turned as it is alone."""
+    f, dt = _freq(64), torch.bfloat16
+    fused = _randn(1, n, h + 2 * g, 64, dtype=dt, seed=h + n)
+    q, k = fused[:, :, :h].transpose(1, 2), fused[:, :, h:h + g].transpose(1, 2)
+    qo, ko = hils.rotate(q, f, k=k)
+    for x, y in ((q, qo), (k, ko)):
+        for i in range(x.shape[1]):
+            assert torch.equal(y[:, i:i + 1], hils.rotate(x[:, i:i + 1], f))
