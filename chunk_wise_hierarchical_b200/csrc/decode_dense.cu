@@ -29,11 +29,13 @@
 //
 // Measured (events around graphs of 20 calls, caches beyond L2, bf16): 8 sequences of 32K, 16
 // heads of 64, 164 us (1.07 GB, 6.6 TB/s); 33 sequences of 0 to 16K, 32 heads over 8 of 128,
-// 172 us (1.13 GB, 6.6 TB/s); one of 512K, the same heads, 313 us (2.15 GB, 6.9 TB/s); 64 of up
-// to 2K 51 us (5.4 TB/s); one of 1013 tokens 6.9 us, a chain of latencies: lengths, block
-// table, copy, one unit's products, ticket, join.  The tensor pipe is 15% busy.  fp32 with one
-// head or few per KV head reads at 6.1 to 6.6 TB/s; with eight it is bound by the CUDA cores
-// (262K of 2 KV heads: 60 us at d = 64, 4.5 TB/s, and 110 us at d = 128, 4.9 TB/s).
+// 171 us (1.13 GB, 6.6 TB/s); one of 512K, the same heads, 311 us (2.15 GB, 6.9 TB/s); 64 of up
+// to 2K 51 us (5.4 TB/s); one of 1013 tokens 7.1 us, a chain of latencies: lengths, block
+// table, copy, one unit's products, ticket, join.  The tensor pipe is 10 to 15% busy.  fp32 with
+// one head or few per KV head reads at 6.1 to 6.6 TB/s.  With eight (262K of 2 KV heads: 61 us at
+// d = 64, 4.4 TB/s, and 111 us at d = 128, 4.8 TB/s) no pipe is full -- FMA 32%, shared memory 41
+// to 49%, an instruction in 47% of the cycles -- but a warp has no copy on its way while it
+// computes, and two warps per scheduler do not cover that.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -53,8 +55,11 @@ constexpr int kDenseThreads = kDenseWarps * 32;
 constexpr int kDenseCtas = 148;          // one per SM
 constexpr int kDenseSeqs = 1024;         // sequences of one launch (their prefix sums in shared memory)
 constexpr int kDenseMaxTiles = 4;        // units of a chunk and KV head, at most
-// Units of a CTA, at least: more SMs for a short context read it sooner and then join more parts
-// (1013 tokens, 8 KV heads of 128: 9.0 us with 2, 7.4 with 4, 9.1 with 8).
+// Units of a CTA, at least: more SMs for a short context read it sooner and then join more parts.
+// Over fifteen short shapes (100 to 32K tokens, 1 to 16 KV heads, both types) 8% more time with 1,
+// 6% with 2, 9% with 8: 100 tokens, 8 KV heads of 128: 6.6, 6.2, 4.7 (4), 5.8 us; 1013 of them
+// 6.9, 6.9, 7.1, 8.1; 8K, one head of 64: 9.2, 8.9, 7.6, 8.0; window of 512 over 7 sequences 8.5,
+// 8.5, 8.6, 9.5.
 constexpr int kDenseMinUnits = 4;
 // Partials joined in one step, one per lane; more (one KV head over up to 148 SMs) are joined in
 // blocks of kJoinBlock first, by different SMs (262K of one KV head, 8 heads of 128: 37 us with
@@ -63,8 +68,9 @@ constexpr int kJoinMost = 32;
 constexpr int kJoinBlock = 13;
 
 // Bytes of a warp's ring: one unit.  Eight warps have 128 KB in flight, which reaches the card's
-// read rate; 192 KB lose some of it again (one 512K context, 7B heads: 306 us with 128 KB, 317 us
-// with 192 KB, in the form with a producer warp), and so do two units of 8 KB (308 and 316 us).
+// read rate; more does not fit beside the partials.  Two units of 8 KB in it are 3% slower over ten
+// shapes (32K of 16 heads: 164 and 169 us; 64 sequences up to 2K: 51 and 55), one of them (64 KB
+// in flight) 8% (164 and 173, 512K: 313 and 352 us).
 constexpr int kDenseRing = 16 * 1024;
 
 // T element, D head dim, G heads per KV head.

@@ -16,9 +16,10 @@
 // a CTA takes kRotThreads / (units per row) of them: short sequences fill it as long ones do.
 // Loads and stores are marked as streaming (nothing is read twice): reads that stayed in L2
 // pushed half-written output lines out of it (345M prefill shape: 55 -> 47 us).  Measured:
-// q and k of the 345M prefill shape, slices of a fused projection, 44 us (268 MB, 6.1 TB/s);
-// fp32 gradients of the 16K training shape 165 us (1.07 GB, 6.5 TB/s); 20K prompt tokens of the
-// 7B shape appended in 80 us (490 MB, 6.1 TB/s); one token for each of 64 sequences 3.6 us.
+// q and k of the 345M prefill shape, slices of a fused projection, 44 us (268 MB, 6.2 TB/s), to
+// fp32 72 us (403 MB, 5.6 TB/s), from fp32 to bf16 63 us (6.4 TB/s); fp32 gradients of the 16K
+// training shape 164 us (1.07 GB, 6.6 TB/s); 20K prompt tokens of the 7B shape appended in 80 us
+// (490 MB, 6.1 TB/s); one token for each of 64 sequences 3.7 us.
 #include "common.cuh"
 #include "kernels.cuh"
 

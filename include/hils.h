@@ -113,9 +113,9 @@ HILS_API int32_t hils_abi_version(void);
 /*
  * hils_set_wait_limit -- sets how many times an ordinary bounded wait of the
  * tensor-core kernels (select, prefill attention) and of the dense decode polls
- * its mbarrier before the kernel gives up.  A kernel that gives up sets the timeout bit of the error
- * word (hils_device_status then returns HILS_ERR_DEVICE_TIMEOUT), stops issuing
- * work, waits for the copies and MMAs it has already issued (those drain waits
+ * its mbarrier before the kernel gives up.  A kernel that gives up sets the
+ * timeout bit of the error word (hils_device_status then returns
+ * HILS_ERR_DEVICE_TIMEOUT), stops issuing work, waits for the copies and MMAs it has already issued (those drain waits
  * always use HILS_DEFAULT_WAIT_LIMIT), releases its tensor memory and returns
  * without writing its outputs; a later call on the same context runs normally.
  * The limit is process-wide and read when a call launches its kernels (a CUDA
@@ -381,8 +381,9 @@ HILS_API hils_status hils_decode_ex(const hils_shape* shape, const void* q, cons
 
 /* Rows of head_dim adjacent elements, one per (batch, head, token):
  * row = data + batch*batch_stride + head*head_stride + token*token_stride, strides in
- * elements, not negative (a dimension of one entry needs none).  data and every stride times the element size are multiples of
- * 16 bytes, so slices of a fused [tokens, (h + 2g) * d] projection are read where they lie.
+ * elements, not negative (a dimension of one entry needs none).  data and every stride times
+ * the element size are multiples of 16 bytes, so slices of a fused [tokens, (h + 2g) * d]
+ * projection are read where they lie.
  * Rows that are written share no element with one another, and lie apart from every other
  * tensor of the call but, where this is said, their own input. */
 typedef struct {
@@ -499,8 +500,8 @@ HILS_API hils_status hils_decode_dense(const hils_shape* shape, const void* q, c
 
 /*
  * hils_device_status -- synchronises `stream`, reads and clears the error
- * word at the start of a hils_attend / hils_attend_selected / hils_decode
- * workspace, and returns HILS_OK, HILS_ERR_DEVICE_CHECK or
+ * word at the start of a workspace of any entry point above that takes one,
+ * and returns HILS_OK, HILS_ERR_DEVICE_CHECK or
  * HILS_ERR_DEVICE_TIMEOUT.  The word is sticky: kernels only set bits, so it
  * reports every error since the last read.  A new workspace must be
  * zero-filled once before its first use.
