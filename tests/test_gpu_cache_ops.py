@@ -9,6 +9,8 @@ Tolerances, derived from the arithmetic (u(t) = eps(t) / 2, half a step of the o
   over n keys n 2^-24.  So each p is off by r = 2 e_s + 2^-16 + n 2^-23 relative (twice e_s:
   the logit and the normaliser), the output by r sum_j p_j |v_j| + u(out) |out|, the
   log-sum-exp by r + 2^-22 |lse|.
+  (The weights now enter in three parts that hold them: 2^-16 is wider than it need be, and the
+  cases at the end on weights and sums are held to less.)
 """
 import ctypes
 import math
